@@ -62,7 +62,9 @@ typedef enum disco_status {
 typedef enum disco_dtype {
     DISCO_F32 = 0,
     DISCO_BF16 = 1,
-    DISCO_F16 = 2
+    DISCO_F16 = 2,
+    DISCO_F8_E4M3 = 3,        /* 8-bit forms (OCP): disco_rms_norm_f8 and disco_dequantize only */
+    DISCO_F8_E5M2 = 4
 } disco_dtype;
 
 /* Host-side CSR filter ("psi").  Rows r = k*Ho + ho, K*Ho rows in all.
@@ -202,6 +204,68 @@ disco_status disco_fused_conv_bwd_saved(disco_psi h, const disco_tensor *out, co
  * race and must not be issued.  The array's contents on entry are ignored. */
 disco_status disco_fused_conv_bwd_noalloc(disco_psi h, const disco_tensor *x, const disco_tensor *W,
                                           const disco_tensor *gy, disco_tensor *gx, disco_tensor *dW, void *stream);
+
+/* ---- the operators around the convolution in a residual model's training step -------------------------
+ *
+ * They take dense tensors of 1 to 5 dimensions and no psi, and run on the current device.  `axis` is the
+ * normalised axis (negative: counted from the end): 1 for fields (B, C, H, W), the last one for rows
+ * (points, C).  D is the axis's size (at least 1).  Tensors need only their element's alignment, so views
+ * into a flat buffer serve.  Outputs must overlap neither inputs nor each other
+ * (DISCO_ERR_INVALID_ARGUMENT).  All statistics are fp32 or wider, each output is rounded once (RNE), and
+ * results are bitwise reproducible run to run.  Nothing is allocated on the device, so every call can be
+ * captured into a graph.  A tensor with no elements is accepted and nothing is launched for it. */
+
+/* Root-mean-square norm over `axis`, of x or, with `residual`, of h = x + residual:
+ *   y = h * rstd * w,   rstd = (mean(h^2) + eps)^(-1/2)
+ * x, residual, y, h: one shape and dtype (F32, BF16 or F16); w: (D,), F32 or that dtype.  With a residual
+ * `h` receives the sum (rounded; the norm itself uses the unrounded fp32 sum); residual and h are given
+ * together or both NULL.  NaN and infinities follow the formula: one in a row makes that row NaN or zero,
+ * and no other. */
+disco_status disco_rms_norm(const disco_tensor *x, const disco_tensor *residual, const disco_tensor *w, int axis,
+                            float eps, disco_tensor *y, disco_tensor *h, void *stream);
+
+/* The same norm with its output in 8 bits: q (x's shape, DISCO_F8_E4M3 or DISCO_F8_E5M2) and fp32 scales,
+ * one for each run of `group` entries along the axis (0: one for the whole axis; else a multiple of 32; the
+ * last run may be shorter):
+ *   scale = max(max|y| over the run / qmax, 2^-126),  q = y / scale rounded (RNE),  qmax = 448 or 57344
+ * from the unrounded fp32 y.  scale: x's shape with the axis replaced by the number of runs.  A NaN in a run
+ * makes its scale and all its q NaN. */
+disco_status disco_rms_norm_f8(const disco_tensor *x, const disco_tensor *residual, const disco_tensor *w, int axis,
+                               float eps, int64_t group, disco_tensor *q, disco_tensor *scale, disco_tensor *h,
+                               void *stream);
+
+/* out = q * scale, the reader of that form: q, scale, axis and group as disco_rms_norm_f8 gives them; out: q's
+ * shape, F32, BF16 or F16. */
+disco_status disco_dequantize(const disco_tensor *q, const disco_tensor *scale, int axis, int64_t group,
+                              disco_tensor *out, void *stream);
+
+/* Backward of disco_rms_norm.  h: the tensor the norm was taken of (the stored sum, or x without a residual),
+ * gy: the gradient of y, gh: the gradient that reaches h past the norm (the residual path) or NULL.  With g = gy * w:
+ *   gx = rstd * g - h * rstd^3 * mean(g h) + gh     (the gradient of x, and of the residual)
+ *   dw = sum over all points of gy * h * rstd
+ * h, gy, gh, gx: one shape and dtype; w, dw: (D,), F32 or that dtype, both alike.  `workspace` is caller-owned
+ * device memory (4-byte aligned) of at least the size disco_rms_norm_bwd_workspace reports for h (its data is not
+ * read); its contents on entry are ignored.  Calls sharing one workspace must not overlap.  With no points
+ * (an empty h) dw is written as zeros. */
+disco_status disco_rms_norm_bwd_workspace(const disco_tensor *h, int axis, size_t *bytes);
+disco_status disco_rms_norm_bwd(const disco_tensor *h, const disco_tensor *w, const disco_tensor *gy,
+                                const disco_tensor *gh, int axis, float eps, disco_tensor *gx, disco_tensor *dw,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* norm = sqrt(sum of the squares of all elements of the n tensors), squares summed in fp64.  The tensors may
+ * differ in shape and dtype (F32, BF16, F16) and may be empty; n may be 0 (norm 0).  norm: one F32 element.
+ * `workspace`: caller-owned device memory (8-byte aligned) of at least the size disco_grad_norm_workspace
+ * reports for these tensors (their data is not read), as disco_rms_norm_bwd's. */
+disco_status disco_grad_norm_workspace(int64_t n, const disco_tensor *grads, size_t *bytes);
+disco_status disco_grad_norm(int64_t n, const disco_tensor *grads, disco_tensor *norm, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Clipping by that norm: outs[i] = grads[i] * min(1, max_norm / (norm + eps)), each rounded once; norm is the
+ * norm before clipping.  outs[i] has the shape and dtype of grads[i] and is either the same memory (in place;
+ * nothing is rewritten where the factor is 1) or disjoint from everything else.  A NaN norm makes every
+ * output NaN, an infinite one makes finite elements 0.  The factor stays on the device. */
+disco_status disco_clip_grads(int64_t n, const disco_tensor *grads, float max_norm, float eps, disco_tensor *outs,
+                              disco_tensor *norm, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Message of the last non-OK status returned on the calling thread ("" if none). */
 const char *disco_last_error(void);

@@ -36,9 +36,13 @@ STATUS_NAMES = {
 DISCO_F32 = 0
 DISCO_BF16 = 1
 DISCO_F16 = 2
+DISCO_F8_E4M3 = 3
+DISCO_F8_E5M2 = 4
 EXPORTED = ("disco_psi_create", "disco_psi_destroy", "disco_fwd", "disco_bwd", "disco_fused_conv",
             "disco_fused_conv_save", "disco_einsum", "disco_fused_conv_bwd_workspace", "disco_fused_conv_bwd",
-            "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc", "disco_last_error")
+            "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc", "disco_rms_norm", "disco_rms_norm_f8",
+            "disco_dequantize", "disco_rms_norm_bwd_workspace", "disco_rms_norm_bwd", "disco_grad_norm_workspace",
+            "disco_grad_norm", "disco_clip_grads", "disco_last_error")
 
 
 class DiscoError(RuntimeError):
@@ -83,10 +87,21 @@ def load_library():
                                                        ctypes.POINTER(ctypes.c_size_t)]
         lib.disco_fused_conv_bwd.argtypes = [P] + [ctypes.POINTER(TensorDesc)] * 5 + [P, ctypes.c_size_t, P]
         lib.disco_fused_conv_bwd_noalloc.argtypes = [P] + [ctypes.POINTER(TensorDesc)] * 5 + [P]
+        T, I64, F, SZ = ctypes.POINTER(TensorDesc), ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        lib.disco_rms_norm.argtypes = [T, T, T, ctypes.c_int, F, T, T, P]
+        lib.disco_rms_norm_f8.argtypes = [T, T, T, ctypes.c_int, F, I64, T, T, T, P]
+        lib.disco_dequantize.argtypes = [T, T, ctypes.c_int, I64, T, P]
+        lib.disco_rms_norm_bwd_workspace.argtypes = [T, ctypes.c_int, ctypes.POINTER(SZ)]
+        lib.disco_rms_norm_bwd.argtypes = [T, T, T, T, ctypes.c_int, F, T, T, P, SZ, P]
+        lib.disco_grad_norm_workspace.argtypes = [I64, P, ctypes.POINTER(SZ)]
+        lib.disco_grad_norm.argtypes = [I64, P, T, P, SZ, P]
+        lib.disco_clip_grads.argtypes = [I64, P, F, F, P, T, P, SZ, P]
         lib.disco_last_error.restype = ctypes.c_char_p
         for f in ("disco_psi_create", "disco_psi_destroy", "disco_fwd", "disco_bwd", "disco_fused_conv",
                   "disco_fused_conv_save", "disco_einsum", "disco_fused_conv_bwd_workspace", "disco_fused_conv_bwd",
-                  "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc"):
+                  "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc", "disco_rms_norm", "disco_rms_norm_f8",
+                  "disco_dequantize", "disco_rms_norm_bwd_workspace", "disco_rms_norm_bwd",
+                  "disco_grad_norm_workspace", "disco_grad_norm", "disco_clip_grads"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -286,3 +301,158 @@ def disco_fused_conv_bwd_saved(psi: Psi, out, W, gy, gx=None, dW=None, workspace
                                                      ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
                                                      _stream(out.device)))
     return gx, dW
+
+
+# ---- the operators around the convolution in a residual model's training step
+
+_CODES = {}  # torch dtype -> disco_dtype
+
+
+def _codes():
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16,
+                       torch.float8_e4m3fn: DISCO_F8_E4M3, torch.float8_e5m2: DISCO_F8_E5M2})
+    return _CODES
+
+
+def _desc(t):
+    """tensor_desc of a tensor of any of the library's types, or None for None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("disco tensors must be contiguous")
+    shape = t.shape
+    return TensorDesc(t.data_ptr(), _codes().get(t.dtype, 99), len(shape), shape[:5])
+
+
+def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
+    """y = h w / sqrt(mean(h^2) + eps) over `axis`, h = x + residual.
+
+    Returns y, or (y, h) with a residual.  axis 1 normalises fields (B, C, H, W) over their channels, -1 rows
+    (points, C); w (D,) is fp32 or of x's type."""
+    import torch
+
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    _check(load_library().disco_rms_norm(_desc(x), _desc(residual), _desc(w), axis, eps, _desc(y), _desc(h),
+                                         _stream(x.device)))
+    return y if residual is None else (y, h)
+
+
+def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None, q=None, scale=None, h=None):
+    """disco_rms_norm with its output in 8 bits: (q, scale), or (q, scale, h) with a residual.
+
+    q is of `dtype` (torch.float8_e4m3fn, the default, or torch.float8_e5m2); scale (fp32) has x's shape with the axis
+    replaced by the number of runs of `group` entries (0: one run, the whole axis; else a multiple of 32)."""
+    import torch
+
+    if q is None:
+        q = torch.empty_like(x, dtype=dtype or torch.float8_e4m3fn)
+    if scale is None:
+        shape = list(x.shape)
+        shape[axis] = -(-shape[axis] // group) if group > 0 else 1
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    _check(load_library().disco_rms_norm_f8(_desc(x), _desc(residual), _desc(w), axis, eps, group, _desc(q),
+                                            _desc(scale), _desc(h), _stream(x.device)))
+    return (q, scale) if residual is None else (q, scale, h)
+
+
+def disco_dequantize(q, scale, dtype=None, axis=1, group=0, out=None):
+    """out = q * scale in `dtype` (default bf16): the reader of disco_rms_norm_f8's form."""
+    import torch
+
+    if out is None:
+        out = torch.empty_like(q, dtype=dtype or torch.bfloat16)
+    _check(load_library().disco_dequantize(_desc(q), _desc(scale), axis, group, _desc(out), _stream(q.device)))
+    return out
+
+
+def disco_rms_norm_bwd_workspace(h, axis=1) -> int:
+    """Workspace bytes disco_rms_norm_bwd needs for this h."""
+    n = ctypes.c_size_t()
+    _check(load_library().disco_rms_norm_bwd_workspace(_desc(h), axis, ctypes.byref(n)))
+    return int(n.value)
+
+
+def disco_rms_norm_bwd(h, w, gy, gh=None, axis=1, eps=1e-6, gx=None, dw=None, workspace=None):
+    """(gx, dw): gradients of disco_rms_norm at h (the stored sum, or x without a residual).
+
+    gh is the gradient that reaches h past the norm; gx is the gradient of x and of the residual alike.  The
+    workspace (a uint8 device tensor) is allocated here when not given."""
+    import torch
+
+    if gx is None:
+        gx = torch.empty_like(h)
+    if dw is None:
+        dw = torch.empty_like(w)
+    lib, d, n = load_library(), _desc(h), ctypes.c_size_t()
+    _check(lib.disco_rms_norm_bwd_workspace(d, axis, n))
+    if workspace is None:
+        workspace = torch.empty(max(n.value, 1), dtype=torch.uint8, device=h.device)
+    _check(lib.disco_rms_norm_bwd(d, _desc(w), _desc(gy), _desc(gh), axis, eps, _desc(gx), _desc(dw),
+                                  workspace.data_ptr(), workspace.numel(), _stream(h.device)))
+    return gx, dw
+
+
+def _flat_descs(tensors):
+    """An array of TensorDesc, each tensor as its elements in a row."""
+    import torch
+
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError("disco tensors must be contiguous")
+    a = np.zeros((max(len(tensors), 1), ctypes.sizeof(TensorDesc) // 8), np.int64)
+    if tensors:
+        a[:, 0] = list(map(torch.Tensor.data_ptr, tensors))
+        codes = _codes()
+        kinds = {t.dtype for t in tensors}
+        if len(kinds) == 1:
+            a[:, 1] = codes.get(kinds.pop(), 99) | 1 << 32
+        else:
+            a[:, 1] = [codes.get(t.dtype, 99) | 1 << 32 for t in tensors]
+        a[:, 2] = list(map(torch.Tensor.numel, tensors))
+    return a
+
+
+def _grads(grads, device):
+    import torch
+
+    grads = list(grads)
+    if device is None:
+        device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    a, n = _flat_descs(grads), ctypes.c_size_t()
+    _check(load_library().disco_grad_norm_workspace(len(grads), a.ctypes.data, n))
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    return grads, a, norm, torch.empty(n.value, dtype=torch.uint8, device=device), device
+
+
+def disco_grad_norm(grads, device=None):
+    """The norm over all elements of all tensors of the list `grads`, as a 0-dimensional fp32 tensor on their device.
+
+    The tensors may differ in shape and type (fp32, bf16, fp16); squares are summed in fp64."""
+    grads, a, norm, ws, device = _grads(grads, device)
+    _check(load_library().disco_grad_norm(len(grads), a.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(),
+                                          _stream(device)))
+    return norm
+
+
+def disco_clip_grads(grads, max_norm, out=None, eps=1e-6, device=None):
+    """Scale all gradients by min(1, max_norm / (norm + eps)), norm = disco_grad_norm(grads); returns that norm.
+
+    In place, or into the tensors of the list `out`.  The factor never leaves the device."""
+    grads, a, norm, ws, device = _grads(grads, device)
+    if out is None:
+        o = a
+    else:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must have one tensor for each gradient")
+        o = _flat_descs(out)
+    _check(load_library().disco_clip_grads(len(grads), a.ctypes.data, max_norm, eps, o.ctypes.data, _desc(norm),
+                                           ws.data_ptr(), ws.numel(), _stream(device)))
+    return norm

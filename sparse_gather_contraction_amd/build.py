@@ -18,7 +18,11 @@ LIB = os.path.join(PKG, "libdisco.so")
 PROBE_LIB = os.path.join(PKG, "libdisco_probes.so")  # microbenchmarks of the device (measurement only)
 
 SOURCES = ["plan.cpp", "plan_fused.cpp", "plan_tile.cpp", "kernels_tile.hip", "disco_api.hip", "kernels_gather.hip", "kernels_staged.hip", "kernels_fused.hip",
-           "kernels_fused_mfma.hip", "kernels_gemm.hip"]
+           "kernels_fused_mfma.hip", "kernels_gemm.hip", "norm_api.hip", "kernels_norm.hip", "kernels_norm_bwd.hip",
+           "kernels_grad.hip"]
+# Built with unaligned memory access: their vectors lie at any element (odd sizes, views into a flat buffer),
+# and they read no LDS at less than its type's alignment.
+UNALIGNED = {"kernels_norm.hip", "kernels_norm_bwd.hip", "kernels_grad.hip"}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -27,14 +31,14 @@ ARCH = "gfx950"
 # reads at 2-byte alignment are kept as 2-byte reads instead of being merged into wide ones.
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         "-Xclang", "-target-feature", "-Xclang", "-unaligned-access-mode",
          "-Wall", "-Wno-unused-function"]
+ALIGNED = ["-Xclang", "-target-feature", "-Xclang", "-unaligned-access-mode"]
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *FLAGS, *([] if os.path.basename(src) in UNALIGNED else ALIGNED), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     out = "\n".join(l for l in r.stdout.splitlines()
                      if "packed-fp32-ops" not in l and "unaligned-access-mode" not in l)

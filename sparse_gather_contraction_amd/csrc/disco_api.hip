@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.hpp"
 #include "disco.h"
 #include "kernels.hpp"
 #include "plan.hpp"
@@ -708,6 +709,19 @@ void *scratch_ptr(int device)
 }
 
 }  // namespace
+
+namespace disco {
+
+disco_status api_fail(disco_status s, const std::string &msg) { return fail(s, msg); }
+disco_status api_check_device(int device) { return check_device(device); }
+
+disco_status api_fail_oom() noexcept
+{
+    g_last_error.clear();
+    return DISCO_ERR_OOM;
+}
+
+}  // namespace disco
 
 extern "C" {
 

@@ -1,0 +1,397 @@
+// kernels_norm_bwd.hip — backward of the root-mean-square norm.
+//
+// With h the stored sum, g = gy w, rstd = (mean_d h^2 + eps)^(-1/2):
+//   gx = rstd g - h rstd^3 mean_d(g h)  (+ gh, the gradient that reaches h past the norm)
+//   dw[d] = sum over all points of gy h rstd
+//
+// Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
+// registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
+// fp32 registers over the workgroup's tiles, then over its lanes, and the workgroups' partial rows are
+// summed in fp64 by a second launch; every order is fixed, so results are bitwise reproducible.
+#include "kernels.hpp"
+#include "norm.hpp"
+#include "norm_device.hpp"
+
+namespace disco {
+
+namespace {
+
+struct BwdArgs {
+    const void *h, *gy, *gh, *w;
+    void *gx;
+    float *partial;
+    int64_t N, M, tiles;
+    int32_t D, wf32, lg, tiles_n;
+    float eps;
+};
+
+// Columns (M > 1): the forward's tiles.  LDS: [parts][P] sums of h^2, [parts][P] of g h, [P] rstd,
+// [P] rstd^3 mean(g h); at the end [waves of one g][channels] of dw.
+template <typename T, int VEC, int CPT, bool RES>
+__global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
+{
+    extern __shared__ float lds[];
+    const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg;
+    const int P = VEC << a.lg, groups = blockDim.x >> a.lg;
+    const int lg6 = a.lg < 6 ? 6 : a.lg, parts = blockDim.x >> lg6, part = t >> lg6;
+    float *s_hh = lds, *s_gh = lds + parts * P, *rs = lds + 2 * parts * P, *cs = rs + P;
+    const int c0 = g * CPT;
+    float w[CPT], acc[CPT];
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+        w[j] = c0 + j < a.D ? load_weight<T>(a.w, a.wf32, c0 + j) : 0.0f;
+        acc[j] = 0.0f;
+    }
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const ColPos pos = col_pos(tile, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
+        const int64_t base = pos.n * a.D * a.M + pos.m;
+        Pack<T, VEC> ph[CPT], pg[CPT], pr[CPT];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            const int64_t o = base + (int64_t)(c0 + j < a.D ? c0 + j : a.D - 1) * a.M;
+            ph[j] = load_pack<T, VEC>((const T *)a.h + o);
+            pg[j] = load_pack<T, VEC>((const T *)a.gy + o);
+        }
+        if constexpr (RES) {
+#pragma unroll
+            for (int j = 0; j < CPT; ++j)
+                pr[j] = load_pack<T, VEC>((const T *)a.gh + base + (int64_t)(c0 + j < a.D ? c0 + j : a.D - 1) * a.M);
+        }
+        float hh[VEC], gh[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) hh[e] = gh[e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            if (c0 + j >= a.D) continue;
+            float h[VEC], gy[VEC];
+            unpack(ph[j], h);
+            unpack(pg[j], gy);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                hh[e] = __builtin_fmaf(h[e], h[e], hh[e]);
+                gh[e] = __builtin_fmaf(gy[e] * w[j], h[e], gh[e]);
+            }
+        }
+        for (int o = 1 << a.lg; o < 64; o <<= 1)  // the wave's threads that hold the same points
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                hh[e] += __shfl_xor(hh[e], o);
+                gh[e] += __shfl_xor(gh[e], o);
+            }
+        if (a.lg >= 6 || (t & 63) < (1 << a.lg))
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                s_hh[part * P + lane * VEC + e] = hh[e];
+                s_gh[part * P + lane * VEC + e] = gh[e];
+            }
+        __syncthreads();
+        for (int p = t; p < P; p += blockDim.x) {
+            float u = 0.0f, v = 0.0f;
+            for (int i = 0; i < parts; ++i) {
+                u += s_hh[i * P + p];
+                v += s_gh[i * P + p];
+            }
+            const float r = rsqrtf(u / (float)a.D + a.eps);
+            rs[p] = r;
+            cs[p] = r * r * r * (v / (float)a.D);
+        }
+        __syncthreads();
+        float rstd[VEC], c[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            rstd[e] = rs[lane * VEC + e];
+            c[e] = cs[lane * VEC + e];
+        }
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            keep_packed(ph[j]);
+            keep_packed(pg[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+            if (c0 + j >= a.D) continue;
+            float h[VEC], gy[VEC], o[VEC];
+            unpack(ph[j], h);
+            unpack(pg[j], gy);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float hr = h[e] * rstd[e];
+                acc[j] = e >= pos.dup ? __builtin_fmaf(gy[e], hr, acc[j]) : acc[j];
+                o[e] = rstd[e] * (gy[e] * w[j]) - h[e] * c[e];
+            }
+            if constexpr (RES) {
+                float r[VEC];
+                unpack(pr[j], r);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] += r[e];
+            }
+            store_f32<T, VEC>((T *)a.gx + base + (int64_t)(c0 + j) * a.M, o);
+        }
+    }
+    const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
+#pragma unroll
+    for (int j = 0; j < CPT; ++j)
+        for (int o = 0; o < in_wave; ++o) acc[j] += __shfl_xor(acc[j], 1 << o);
+    __syncthreads();
+    if ((lane & ((1 << in_wave) - 1)) == 0)
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) lds[(lane >> 6) * width + c0 + j] = acc[j];
+    __syncthreads();
+    for (int c = t; c < a.D; c += blockDim.x) {
+        float s = lds[c];
+        for (int i = 1; i < waves; ++i) s += lds[i * width + c];
+        a.partial[(int64_t)blockIdx.x * a.D + c] = s;
+    }
+}
+
+struct Sum2 {
+    float u, v;
+};
+
+// Two sums over the 2^lg threads of a row.
+__device__ __forceinline__ Sum2 row_sum2(Sum2 s, int lg, Sum2 *slots)
+{
+    const int in_wave = lg < 6 ? lg : 6;
+    for (int o = 0; o < in_wave; ++o) {
+        s.u += __shfl_xor(s.u, 1 << o);
+        s.v += __shfl_xor(s.v, 1 << o);
+    }
+    if (lg > 6) {  // uniform over the workgroup
+        const int wave = threadIdx.x >> 6, per_row = 1 << (lg - 6), first = wave & ~(per_row - 1);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) slots[wave] = s;
+        __syncthreads();
+        s = slots[first];
+        for (int i = 1; i < per_row; ++i) {
+            s.u += slots[first + i].u;
+            s.v += slots[first + i].v;
+        }
+    }
+    return s;
+}
+
+// Rows (M = 1).  Dynamic LDS: [rows][D] for the join of dw where a workgroup holds several rows.
+template <typename T, int VEC, int KPT, bool RES>
+__global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
+{
+    extern __shared__ float lds[];
+    __shared__ Sum2 slots[kNormMaxThreads / 64];
+    const int t = threadIdx.x, lanes = 1 << a.lg, tt = t & (lanes - 1), slot = t >> a.lg;
+    const int rows = blockDim.x >> a.lg;
+    RowPos pos[KPT];
+    float w[KPT][VEC], acc[KPT][VEC];
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+        pos[k] = row_pos(k * lanes + tt, VEC, a.D);
+        if (a.wf32) load_f32<float, VEC>((const float *)a.w + pos[k].c, w[k]);
+        else load_f32<T, VEC>((const T *)a.w + pos[k].c, w[k]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[k][e] = 0.0f;
+    }
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const int64_t want = tile * rows + slot;
+        const bool live = want < a.N;
+        const int64_t base = (live ? want : a.N - 1) * a.D;  // a slot past the end repeats the last row
+        Pack<T, VEC> ph[KPT], pg[KPT], pr[KPT];
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            ph[k] = load_pack<T, VEC>((const T *)a.h + base + pos[k].c);
+            pg[k] = load_pack<T, VEC>((const T *)a.gy + base + pos[k].c);
+            if constexpr (RES) pr[k] = load_pack<T, VEC>((const T *)a.gh + base + pos[k].c);
+        }
+        Sum2 s = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            float h[VEC], gy[VEC];
+            unpack(ph[k], h);
+            unpack(pg[k], gy);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= pos[k].dup) {
+                    s.u = __builtin_fmaf(h[e], h[e], s.u);
+                    s.v = __builtin_fmaf(gy[e] * w[k][e], h[e], s.v);
+                }
+        }
+        s = row_sum2(s, a.lg, slots);
+        const float rstd = rsqrtf(s.u / (float)a.D + a.eps), c = rstd * rstd * rstd * (s.v / (float)a.D);
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            keep_packed(ph[k]);
+            keep_packed(pg[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            if (pos[k].dup >= VEC) continue;
+            float h[VEC], gy[VEC], o[VEC];
+            unpack(ph[k], h);
+            unpack(pg[k], gy);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float hr = h[e] * rstd;
+                acc[k][e] = live && e >= pos[k].dup ? __builtin_fmaf(gy[e], hr, acc[k][e]) : acc[k][e];
+                o[e] = rstd * (gy[e] * w[k][e]) - h[e] * c;
+            }
+            if constexpr (RES) {
+                float r[VEC];
+                unpack(pr[k], r);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) o[e] += r[e];
+            }
+            store_f32<T, VEC>((T *)a.gx + base + pos[k].c, o);
+        }
+    }
+    float *mine = a.partial + (int64_t)blockIdx.x * a.D;
+    if (rows > 1) {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= pos[k].dup) lds[slot * a.D + pos[k].c + e] = acc[k][e];
+        __syncthreads();
+        for (int c = t; c < a.D; c += blockDim.x) {
+            float s = 0.0f;
+            for (int i = 0; i < rows; ++i) s += lds[i * a.D + c];
+            mine[c] = s;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= pos[k].dup) mine[pos[k].c + e] = acc[k][e];
+    }
+}
+
+// More channels than registers hold: the threads walk the channels twice, and the workgroup's row of
+// partial sums is kept in device memory, each entry by one thread.
+template <typename T, bool RES>
+__global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
+{
+    extern __shared__ float lds[];
+    const int t = threadIdx.x, P = 1 << a.lg, lane = t & (P - 1), g = t >> a.lg, groups = blockDim.x >> a.lg;
+    float *s_hh = lds, *s_gh = lds + groups * P;
+    float *mine = a.partial + (int64_t)blockIdx.x * a.D;
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const ColPos pos = col_pos(tile, lane, 1, a.lg, 0, a.N, a.M);
+        const int64_t base = pos.n * a.D * a.M + pos.m;
+        const T *hp = (const T *)a.h + base, *gp = (const T *)a.gy + base;
+        float hh = 0.0f, gh = 0.0f;
+        for (int c = g; c < a.D; c += groups) {
+            const float h = load_elem(hp, (int64_t)c * a.M), gy = load_elem(gp, (int64_t)c * a.M);
+            hh = __builtin_fmaf(h, h, hh);
+            gh = __builtin_fmaf(gy * load_weight<T>(a.w, a.wf32, c), h, gh);
+        }
+        __syncthreads();
+        s_hh[g * P + lane] = hh;
+        s_gh[g * P + lane] = gh;
+        __syncthreads();
+        for (int o = groups >> 1; o > 0; o >>= 1) {  // `groups` is a power of two
+            if (g < o) {
+                s_hh[g * P + lane] += s_hh[(g + o) * P + lane];
+                s_gh[g * P + lane] += s_gh[(g + o) * P + lane];
+            }
+            __syncthreads();
+        }
+        const float rstd = rsqrtf(s_hh[lane] / (float)a.D + a.eps);
+        const float k = rstd * rstd * rstd * (s_gh[lane] / (float)a.D);
+        for (int c = g; c < a.D; c += groups) {
+            const float h = load_elem(hp, (int64_t)c * a.M), gy = load_elem(gp, (int64_t)c * a.M);
+            float o = rstd * (gy * load_weight<T>(a.w, a.wf32, c)) - h * k;
+            if constexpr (RES) o += load_elem((const T *)a.gh + base, (int64_t)c * a.M);
+            store_elem((T *)a.gx + base, (int64_t)c * a.M, o);
+            float d = pos.dup ? 0.0f : gy * (h * rstd);
+            for (int i = 1; i < P; i <<= 1) d += __shfl_xor(d, i);  // P <= 64 lanes of one wave walk together
+            if (lane == 0) mine[c] = tile == blockIdx.x ? d : mine[c] + d;
+        }
+    }
+}
+
+// dw[c] = the sum of partial[0..blocks)[c]: 16 columns a workgroup, 64 threads a column, fp64.
+template <typename O>
+__global__ __launch_bounds__(1024) void dw_sum_kernel(const float *partial, int blocks, int D, O *dw)
+{
+    __shared__ double part[64][16];
+    const int col = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
+    double s = 0.0;
+    if (c < D) {
+#pragma unroll 4
+        for (int i = r0; i < blocks; i += 64) s += (double)partial[(int64_t)i * D + c];
+    }
+    part[r0][col] = s;
+    __syncthreads();
+    for (int o = 32; o > 0; o >>= 1) {
+        if (r0 < o) part[r0][col] += part[r0 + o][col];
+        __syncthreads();
+    }
+    if (r0 == 0 && c < D) store_elem(dw, c, (float)part[0][col]);
+}
+
+template <typename T, bool RES>
+hipError_t launch_t(const BwdArgs &a, const NormGeom &g, int blocks, hipStream_t s)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    const dim3 grid(blocks), block(g.threads);
+    const size_t lds = norm_bwd_lds(g, a.D);
+#define ROWS(VEC, KPT) bwd_rows_kernel<T, VEC, KPT, RES><<<grid, block, lds, s>>>(a)
+#define COLS(VEC, CPT) bwd_cols_kernel<T, VEC, CPT, RES><<<grid, block, lds, s>>>(a)
+    if (g.loop) {
+        bwd_loop_kernel<T, RES><<<grid, block, lds, s>>>(a);
+    } else if (g.rows) {
+        if (g.vec == 1) ROWS(1, 1);
+        else if (g.per == 1) ROWS(V, 1);
+        else if (g.per == 2) ROWS(V, 2);
+        else ROWS(V, 4);
+    } else if (g.vec == 1) {
+        if (g.per == 1) COLS(1, 1);
+        else if (g.per == 2) COLS(1, 2);
+        else COLS(1, 4);
+    } else {
+        if (g.per == 1) COLS(V, 1);
+        else if (g.per == 2) COLS(V, 2);
+        else COLS(V, 4);
+    }
+#undef ROWS
+#undef COLS
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_r(const BwdArgs &a, const NormGeom &g, bool res, int blocks, hipStream_t s)
+{
+    return res ? launch_t<T, true>(a, g, blocks, s) : launch_t<T, false>(a, g, blocks, s);
+}
+
+}  // namespace
+
+// 256 CUs; 1024 threads of these kernels' registers a CU.
+int32_t norm_bwd_blocks(int64_t N, int64_t D, int64_t M, int esz)
+{
+    if (N == 0 || M == 0) return 0;
+    const NormGeom g = norm_geom(N, D, M, esz, true);
+    const int64_t most = 256 * (g.threads >= 1024 ? 1 : 1024 / g.threads);
+    return (int32_t)(g.tiles < most ? g.tiles : most);
+}
+
+hipError_t launch_norm_bwd(const NormLaunch &l, hipStream_t s)
+{
+    const int esz = l.dtype == 0 ? 4 : 2;
+    if (l.blocks > 0) {
+        const NormGeom g = norm_geom(l.N, l.D, l.M, esz, true);
+        BwdArgs a;
+        a.h = l.x; a.gy = l.gy; a.gh = l.r; a.w = l.w; a.gx = l.y; a.partial = l.partial;
+        a.N = l.N; a.M = l.M; a.tiles = g.tiles;
+        a.D = (int32_t)l.D; a.wf32 = l.wf32; a.lg = g.lg; a.tiles_n = g.tiles_n; a.eps = l.eps;
+        const bool res = l.r != nullptr;
+        const hipError_t e = l.dtype == 0 ? launch_r<float>(a, g, res, l.blocks, s)
+                           : l.dtype == 1 ? launch_r<bf16_t>(a, g, res, l.blocks, s)
+                                          : launch_r<f16_t>(a, g, res, l.blocks, s);
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid((uint32_t)ceil_div64(l.D, 16));
+    if (l.wf32) dw_sum_kernel<float><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (float *)l.dw);
+    else if (l.dtype == 1) dw_sum_kernel<bf16_t><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (bf16_t *)l.dw);
+    else dw_sum_kernel<f16_t><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (f16_t *)l.dw);
+    return hipGetLastError();
+}
+
+}  // namespace disco

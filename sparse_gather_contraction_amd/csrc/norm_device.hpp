@@ -1,0 +1,227 @@
+// norm_device.hpp — vector loads, stores and conversions of the norm, 8-bit and gradient kernels.
+#pragma once
+
+#include "common.hpp"
+
+namespace disco {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// VEC elements of T as they lie in memory.  Loads and stores need the element's alignment only.
+template <typename T, int VEC>
+struct Pack {
+    static constexpr int kBytes = VEC * (int)sizeof(T);
+    static constexpr int kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
+{
+    constexpr int B = Pack<T, VEC>::kBytes;
+    Pack<T, VEC> r;
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) {
+            u32x4 v;
+            __builtin_memcpy(&v, p + i * (16 / (int)sizeof(T)), 16);
+            r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (B == 8) {
+        u32x2 v;
+        __builtin_memcpy(&v, p, 8);
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else if constexpr (B == 4) {
+        __builtin_memcpy(&r.w[0], p, 4);
+    } else if constexpr (B == 2) {
+        r.w[0] = *(const uint16_t *)p;
+    } else {
+        static_assert(B == 1, "pack size");
+        r.w[0] = *(const uint8_t *)p;
+    }
+    return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &r)
+{
+    constexpr int B = Pack<T, VEC>::kBytes;
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) {
+            const u32x4 v = {r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
+            __builtin_memcpy(p + i * (16 / (int)sizeof(T)), &v, 16);
+        }
+    } else if constexpr (B == 8) {
+        const u32x2 v = {r.w[0], r.w[1]};
+        __builtin_memcpy(p, &v, 8);
+    } else if constexpr (B == 4) {
+        __builtin_memcpy(p, &r.w[0], 4);
+    } else if constexpr (B == 2) {
+        *(uint16_t *)p = (uint16_t)r.w[0];
+    } else {
+        *(uint8_t *)p = (uint8_t)r.w[0];
+    }
+}
+
+// Keeps the values as they lie, in their registers: what is unpacked after this is not the fp32 values
+// unpacked before it, which would hold twice the registers of 16-bit elements.
+template <typename T, int VEC>
+__device__ __forceinline__ void keep_packed(Pack<T, VEC> &r)
+{
+    if constexpr (sizeof(T) == 2 && VEC > 1)
+#pragma unroll
+        for (int i = 0; i < Pack<T, VEC>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
+template <int VEC>
+__device__ __forceinline__ void unpack(const Pack<float, VEC> &r, float (&f)[VEC])
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(r.w[i]);
+}
+
+template <int VEC>
+__device__ __forceinline__ void unpack(const Pack<bf16_t, VEC> &r, float (&f)[VEC])
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        f[i] = __uint_as_float((i & 1) ? (r.w[i / 2] & 0xffff0000u) : (r.w[i / 2] << 16));
+}
+
+template <int VEC>
+__device__ __forceinline__ void unpack(const Pack<f16_t, VEC> &r, float (&f)[VEC])
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const f16x2 h = __builtin_bit_cast(f16x2, r.w[i / 2]);
+        f[i] = (float)((i & 1) ? h.y : h.x);
+    }
+}
+
+// fp32 -> the element type, each value rounded once (round to nearest even)
+template <int VEC>
+__device__ __forceinline__ void pack(const float (&f)[VEC], Pack<float, VEC> &r)
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.w[i] = __float_as_uint(f[i]);
+}
+
+template <int VEC>
+__device__ __forceinline__ void pack(const float (&f)[VEC], Pack<bf16_t, VEC> &r)
+{
+    if constexpr (VEC == 1) {
+        r.w[0] = f32_to_bf16(f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const f32x2 v = {f[2 * i], f[2 * i + 1]};
+            r.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void pack(const float (&f)[VEC], Pack<f16_t, VEC> &r)
+{
+    if constexpr (VEC == 1) {
+        r.w[0] = __builtin_bit_cast(uint16_t, (f16_t)f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const f32x2 v = {f[2 * i], f[2 * i + 1]};
+            r.w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+        }
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_f32(const T *p, float (&f)[VEC])
+{
+    unpack(load_pack<T, VEC>(p), f);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_f32(T *p, const float (&f)[VEC])
+{
+    Pack<T, VEC> r;
+    pack(f, r);
+    store_pack<T, VEC>(p, r);
+}
+
+// 8-bit values (fmt 0: e4m3, 1: e5m2, both with the OCP encodings gfx950 converts to), round to nearest even
+template <int VEC>
+__device__ __forceinline__ void pack_f8(const float (&f)[VEC], int fmt, Pack<uint8_t, VEC> &r)
+{
+    if constexpr (VEC == 1) {
+        const int v = fmt ? __builtin_amdgcn_cvt_pk_bf8_f32(f[0], 0.0f, 0, false)
+                          : __builtin_amdgcn_cvt_pk_fp8_f32(f[0], 0.0f, 0, false);
+        r.w[0] = (uint32_t)v & 0xffu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            int v = 0;
+            if (fmt) {
+                v = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * i], f[4 * i + 1], v, false);
+                v = __builtin_amdgcn_cvt_pk_bf8_f32(f[4 * i + 2], f[4 * i + 3], v, true);
+            } else {
+                v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], v, false);
+                v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], v, true);
+            }
+            r.w[i] = (uint32_t)v;
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void unpack_f8(const Pack<uint8_t, VEC> &r, int fmt, float (&f)[VEC])
+{
+    if constexpr (VEC == 1) {
+        const f32x2 v = fmt ? __builtin_amdgcn_cvt_pk_f32_bf8((int)r.w[0], false)
+                            : __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[0], false);
+        f[0] = v.x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const f32x2 a = fmt ? __builtin_amdgcn_cvt_pk_f32_bf8((int)r.w[i], false)
+                                : __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], false);
+            const f32x2 b = fmt ? __builtin_amdgcn_cvt_pk_f32_bf8((int)r.w[i], true)
+                                : __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], true);
+            f[4 * i] = a.x; f[4 * i + 1] = a.y; f[4 * i + 2] = b.x; f[4 * i + 3] = b.y;
+        }
+    }
+}
+
+// The norm's weight, fp32 or of the data type.
+template <typename T>
+__device__ __forceinline__ float load_weight(const void *w, int wf32, int64_t c)
+{
+    return wf32 ? ((const float *)w)[c] : load_elem((const T *)w, c);
+}
+
+// |v| as an unsigned whole number: ordered like the values, with infinity and then NaN above them, so that
+// a maximum over it keeps a NaN.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// scale of a group whose largest |y| is amax: amax / qmax, at least 2^-126 (the reciprocal of a smaller one
+// leaves fp32's range); a NaN stays one
+__device__ __forceinline__ float f8_scale(float amax, float qmax)
+{
+    const float s = amax / qmax;
+    return s < 0x1p-126f ? 0x1p-126f : s;
+}
+
+// y / scale rounded once: the product with the reciprocal, corrected by its residual.  An infinite or NaN
+// scale takes the division itself (0 * inf would turn a quotient of 0 into NaN).
+__device__ __forceinline__ float f8_quot(float y, float scale, float inv)
+{
+    const float q = y * inv;
+    const float e = __builtin_fmaf(-q, scale, y);
+    return __builtin_fmaf(e, inv, q);
+}
+
+}  // namespace disco

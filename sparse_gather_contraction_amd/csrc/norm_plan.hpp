@@ -1,0 +1,204 @@
+// norm_plan.hpp — launch geometry and index arithmetic of the norm kernels (host and device).
+//
+// A tensor is seen as (N, D, M): N the product of the sizes before the normalised axis, D that axis, M
+// the product of the sizes after it; element (n, d, m) lies at (n D + d) M + m.  Two layouts of work:
+//   columns (M > 1): a workgroup holds a tile of P consecutive points (n, m) with all their D channels;
+//     thread (g, lane) holds channels g*per .. g*per+per-1 of the points lane*vec .. lane*vec+vec-1.
+//   rows (M = 1): `lanes` threads hold one row, thread t the vectors t, t + lanes, ... of `vec` elements.
+// A vector that would pass the end of its run is moved back to end there; `dup` says how many of its
+// leading elements are held twice.  So every access is a whole vector inside the tensor, at any size.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#if defined(__HIPCC__)
+#define DISCO_HD __host__ __device__ __forceinline__
+#else
+#define DISCO_HD inline
+#endif
+
+namespace disco {
+
+struct NormGeom {
+    int32_t rows = 0;      // 1: rows layout
+    int32_t loop = 0;      // 1: the channels pass the threads' registers; the looping kernels
+    int32_t vec = 1;       // elements of one load
+    int32_t per = 1;       // columns: channels a thread; rows: vectors a thread
+    int32_t lg = 0;        // log2 of the lanes along the points (columns) or along the row (rows)
+    int32_t groups = 1;    // columns: threads along the channels; rows: rows a workgroup holds at a time
+    int32_t threads = 64;
+    int64_t tiles = 0;     // tiles of points or of rows
+    int32_t tiles_n = 1;   // columns, vec > 1: tiles of one n
+};
+
+DISCO_HD int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- columns
+
+struct ColPos {
+    int64_t n, m;   // the first point held
+    int32_t dup;    // leading elements held by another lane too (vec or more: all of them)
+};
+
+// Where lane `lane` of tile `tile` lies (vec points from m on; flat tiles, vec == 1, run over n too).
+DISCO_HD ColPos col_pos(int64_t tile, int lane, int vec, int lg, int32_t tiles_n, int64_t N, int64_t M)
+{
+    ColPos p;
+    if (vec > 1) {
+        p.n = (int64_t)((uint32_t)tile / (uint32_t)tiles_n);
+        const int64_t m = ((tile - p.n * tiles_n) << lg) * vec + (int64_t)lane * vec;
+        p.m = m < M - vec ? m : M - vec;
+        p.dup = (int32_t)(m - p.m < vec ? m - p.m : vec);
+    } else {
+        const int64_t q = (tile << lg) + lane, last = N * M - 1;
+        const int64_t r = q < last ? q : last;
+        p.n = r / M;
+        p.m = r - p.n * M;
+        p.dup = q > last;
+    }
+    return p;
+}
+
+// ---- rows
+
+struct RowPos {
+    int32_t c;      // first element held
+    int32_t dup;    // leading elements held by another thread too (vec or more: all of them)
+};
+
+DISCO_HD RowPos row_pos(int v, int vec, int D)
+{
+    const int64_t c = (int64_t)v * vec;
+    RowPos p;
+    p.c = (int32_t)(c < D - vec ? c : D - vec);
+    p.dup = (int32_t)(c - p.c < vec ? c - p.c : vec);
+    return p;
+}
+
+// ---- geometry
+
+constexpr int kNormMaxThreads = 1024;
+constexpr int kColsMinM = 64;    // fewer points after the axis than this: flat tiles of single elements
+
+inline int log2_up(int64_t v)
+{
+    int l = 0;
+    while (((int64_t)1 << l) < v) ++l;
+    return l;
+}
+
+// Geometry for (N, D, M) with elements of esz bytes.  N, D, M >= 1.
+inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
+{
+    NormGeom g;
+    const int vmax = 16 / esz;
+    if (M == 1) {
+        g.rows = 1;
+        g.vec = D >= vmax ? vmax : 1;
+        const int64_t nv = ceil_div64(D, g.vec);
+        if (nv > (int64_t)kNormMaxThreads * 4) {
+            g.loop = 1;
+        } else {
+            g.per = nv > 512 ? 4 : nv > 32 ? 2 : 1;
+            g.lg = log2_up(ceil_div64(nv, g.per));
+            const int lanes = 1 << g.lg;
+            g.threads = lanes > 256 ? lanes : 256;
+            g.groups = g.threads / lanes;
+            g.tiles = ceil_div64(N, g.groups);
+            return g;
+        }
+    } else {
+        const bool flat = M < kColsMinM;
+        g.vec = flat ? 1 : vmax;
+        // channels a thread; lanes along the points: a run of 256 bytes, or fewer where the channels need the threads
+        const int pmax = bwd ? 4 : 8;
+        g.per = D >= pmax * 2 ? pmax : D >= 8 ? 4 : D >= 4 ? 2 : 1;
+        const int64_t ng = ceil_div64(D, g.per);
+        int lg = flat ? 6 : 4;
+        while (lg < 8 && (ng << lg) < 256) ++lg;
+        while (lg > 2 && (ng << lg) > kNormMaxThreads) --lg;
+        if ((ng << lg) > kNormMaxThreads) {
+            g.loop = 1;
+        } else {
+            g.lg = lg;
+            int64_t th = ng << lg;
+            th = (th + 63) & ~(int64_t)63;
+            g.threads = (int32_t)th;
+            g.groups = (int32_t)(th >> lg);
+        }
+    }
+    if (g.loop) {
+        // one point (rows) or 32 points at a time; the threads walk the channels
+        g.rows = 0;
+        g.vec = 1;
+        g.per = 1;
+        g.lg = M == 1 ? 0 : 5;
+        g.threads = kNormMaxThreads;
+        g.groups = g.threads >> g.lg;
+    }
+    const int64_t P = ((int64_t)1 << g.lg) * g.vec;
+    if (g.vec > 1) {
+        g.tiles_n = (int32_t)ceil_div64(M, P);
+        g.tiles = (int64_t)g.tiles_n * N;
+    } else {
+        g.tiles = ceil_div64(N * M, P);
+    }
+    return g;
+}
+
+// Columns: partial sums of one point that a workgroup joins through LDS (one a wave, or one a g where the
+// lanes of a g fill whole waves).
+inline int cols_parts(const NormGeom &g) { return g.threads >> (g.lg < 6 ? 6 : g.lg); }
+
+// Dynamic LDS of the forward (ngroups: scales along the axis, 0 without an 8-bit output) and of the backward.
+inline size_t norm_lds(const NormGeom &g, int ngroups)
+{
+    const size_t P = ((size_t)1 << g.lg) * g.vec;
+    if (g.loop) return (g.groups + 1) * P * 4;
+    if (g.rows) return ngroups > 1 ? (size_t)g.groups * ngroups * 4 : 0;
+    return (size_t)(cols_parts(g) + 1 + ngroups) * P * 4;
+}
+
+inline size_t norm_bwd_lds(const NormGeom &g, int64_t D)
+{
+    const size_t P = ((size_t)1 << g.lg) * g.vec;
+    if (g.loop) return 2 * g.groups * P * 4;
+    if (g.rows) return g.groups > 1 ? (size_t)g.groups * D * 4 : 0;
+    const size_t join = (size_t)(2 * cols_parts(g) + 2) * P * 4;
+    const size_t last = (size_t)(g.lg > 6 ? 1 << (g.lg - 6) : 1) * g.groups * g.per * 4;
+    return join > last ? join : last;
+}
+
+// ---- reader of the 8-bit form
+
+constexpr int kDequantCpt = 8;   // columns: channels a thread
+
+struct DequantGeom {
+    bool vec = false;
+    int32_t lg = 6;        // log2 of the lanes along the points (columns) or along the row (rows)
+    int32_t chunks = 1;    // columns: workgroups along the channels
+    int32_t tiles_n = 0;
+    int64_t blocks = 0;    // of 256 threads
+};
+
+inline DequantGeom dequant_geom(int64_t N, int64_t D, int64_t M, int esz)
+{
+    const int V = 16 / esz;
+    DequantGeom g;
+    if (M == 1) {
+        g.vec = D >= V;
+        const int lg = log2_up(ceil_div64(D, g.vec ? V : 1));
+        g.lg = lg < 8 ? lg : 8;
+        g.blocks = ceil_div64(N, 256 >> g.lg);
+    } else {
+        g.vec = M >= kColsMinM;
+        const int64_t P = (int64_t)64 * (g.vec ? V : 1);
+        g.chunks = (int32_t)ceil_div64(D, 4 * kDequantCpt);
+        g.tiles_n = g.vec ? (int32_t)ceil_div64(M, P) : 0;
+        g.blocks = (g.vec ? N * g.tiles_n : ceil_div64(N * M, P)) * g.chunks;
+    }
+    return g;
+}
+
+}  // namespace disco

@@ -1,0 +1,359 @@
+"""The operators around the convolution in a training step (norm, 8-bit norm and its reader, norm backward, gradient
+norm and clipping) against their formulas in fp64.
+
+Bounds.  u = 2^-24 is half a step of fp32, half(t) half a step of the output's type, both relative.  A sum of fp32 terms
+along a chain of n additions is off by at most n u times the sum of the terms' sizes; the kernels' chains (a thread's
+terms, the lanes, the workgroup's parts) are shorter than 80 for every size used here.  So the mean of squares is
+off by 80 u, its inverse root by 40 u and 2 u of its own, y by 45 u and the rounding of the output; the other bounds
+count the same way beside each check.  fp16 results below its normal range are off by up to 2^-25 beside that."""
+import math
+
+import pytest
+import torch
+
+import sparse_gather_contraction_amd as sgc
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+T = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+F8 = {"e4m3": (torch.float8_e4m3fn, 448.0, 2.0 ** -4, 2.0 ** -10), "e5m2": (torch.float8_e5m2, 57344.0, 2.0 ** -3, 2.0 ** -17)}
+U = 2.0 ** -24
+EPS = 1e-6
+
+
+def half(dt):
+    return torch.finfo(dt).eps / 2
+
+
+def floor_of(dt):
+    return 2.0 ** -25 if dt == torch.float16 else 1e-40
+
+
+def randn(shape, dt, seed, std=1.0, shift=0):
+    """A tensor that starts `shift` elements into its storage."""
+    g = torch.Generator().manual_seed(seed)
+    n = math.prod(shape)
+    flat = (torch.randn(n + shift, generator=g) * std).to(dt).to(DEV)
+    return flat[shift:].view(shape)
+
+
+def per(w, x, axis):
+    s = [1] * x.dim()
+    s[axis] = -1
+    return w.view(s)
+
+
+def close(got, ref, bound, what):
+    got = got.double()
+    assert got.shape == ref.shape
+    assert bool(torch.isfinite(got).all()), what + ": non-finite"
+    worst = float(((got - ref).abs() / bound).max()) if got.numel() else 0.0
+    assert worst <= 1.0, f"{what}: {worst} times its bound"
+
+
+SHAPES = [  # (shape, axis): fields with aligned, odd and tiny grids, rows of every kind, middle axes
+    ((1, 1), -1), ((3, 5), -1), ((1, 256), -1), ((67, 8), -1), ((5, 9), -1), ((33, 260), -1), ((129, 512), -1), ((17, 1000), -1),
+    ((9, 1025), -1), ((5, 2048), -1), ((3, 4100), -1), ((3, 8191), -1), ((2, 16385), -1), ((2, 70001), -1), ((1029, 7), -1),
+    ((2, 1, 8, 16), 1), ((2, 3, 5, 7), 1), ((1, 8, 1, 1), 1), ((3, 73, 9, 11), 1), ((2, 32, 18, 36), 1), ((1, 80, 13, 41), 1),
+    ((2, 256, 8, 17), 1), ((1, 257, 3, 43), 1), ((1, 512, 9, 16), 1), ((1, 1000, 8, 9), 1), ((1, 2048, 8, 8), 1), ((1, 2500, 5, 13), 1),
+    ((300, 4, 3), 1), ((64, 33, 2), 1), ((4, 6, 50), 0), ((2, 3, 40, 5), 2), ((70,), 0), ((2, 16, 4, 5, 6), 1), ((1, 32, 400, 333), 1),
+]
+
+
+def ids(v):
+    return "x".join(map(str, v[0])) + f"@{v[1]}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", SHAPES, ids=ids)
+def test_norm(case, dtype):
+    shape, axis = case
+    dt = T[dtype]
+    for shift, residual, wdt in ((0, True, torch.float32), (1, False, dt)):
+        print(f"[norm] {shape} axis {axis} {dtype} shift {shift} residual {residual}", flush=True)
+        x, r = randn(shape, dt, 1, 2.0, shift), randn(shape, dt, 2, 1.0, shift) if residual else None
+        w = randn((shape[axis],), wdt, 3, 1.0, shift)
+        got = sgc.disco_rms_norm(x, w, residual=r, axis=axis, eps=EPS)
+        y, h = got if residual else (got, None)
+        H = x.double() + (r.double() if residual else 0)
+        ref = H * (H.square().mean(axis, keepdim=True) + EPS).rsqrt() * per(w.double(), x, axis)
+        close(y, ref, ref.abs() * (half(dt) + 46 * U) * 1.001 + floor_of(dt), "y")
+        if residual:
+            close(h, H, H.abs() * (half(dt) + U) * 1.001 + floor_of(dt), "h")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", SHAPES, ids=ids)
+def test_norm_f8_and_reader(case, dtype):
+    shape, axis = case
+    dt = T[dtype]
+    D = shape[axis]
+    for shift, residual, f8, group in ((0, True, "e4m3", 0), (1, False, "e4m3", 128), (0, False, "e5m2", 32), (1, True, "e4m3", 96)):
+        print(f"[f8] {shape} axis {axis} {dtype} shift {shift} residual {residual} {f8} group {group}", flush=True)
+        qt, qmax, qhalf, qfloor = F8[f8]
+        x, r = randn(shape, dt, 11, 2.0, shift), randn(shape, dt, 12, 1.0, shift) if residual else None
+        w = randn((D,), torch.float32, 13, 1.0, shift)
+        got = sgc.disco_rms_norm_f8(x, w, residual=r, axis=axis, eps=EPS, group=group, dtype=qt)
+        q, scale = got[0], got[1]
+        H = x.double() + (r.double() if residual else 0)
+        if residual:
+            close(got[2], H, H.abs() * (half(dt) + U) * 1.001 + floor_of(dt), "h")
+        Y = H * (H.square().mean(axis, keepdim=True) + EPS).rsqrt() * per(w.double(), x, axis)
+        g = group or D
+        for k, (ys, qs) in enumerate(zip(Y.split(g, axis), q.float().split(g, axis))):
+            ref = (ys.abs().amax(axis, keepdim=True) / qmax).clamp(min=2.0 ** -126)
+            mine = scale.narrow(axis, k, 1)
+            close(mine, ref, ref * 48 * U, "scale")  # y's 46 u, the quotient's rounding
+            v = ys / ref
+            close(qs, v, v.abs() * (qhalf + 100 * U) + qfloor, "q")  # y and scale perturb v by 96 u
+            for out in (torch.float32, torch.bfloat16, torch.float16):
+                back = sgc.disco_dequantize(q, scale, dtype=out, axis=axis, group=group).narrow(axis, k * g, ys.shape[axis])
+                ref2 = qs.double() * mine.double()
+                close(back, ref2, ref2.abs() * half(out) * 1.001 + floor_of(out), "reader")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", SHAPES, ids=ids)
+def test_norm_bwd(case, dtype):
+    shape, axis = case
+    dt = T[dtype]
+    for shift, with_gh, wdt in ((0, True, dt), (1, False, torch.float32)):
+        print(f"[bwd] {shape} axis {axis} {dtype} shift {shift} gh {with_gh}", flush=True)
+        h, gy = randn(shape, dt, 21, 2.0, shift), randn(shape, dt, 22, 1.0, shift)
+        gh = randn(shape, dt, 23, 1.0, shift) if with_gh else None
+        w = randn((shape[axis],), wdt, 24, 1.0, shift)
+        gx, dw = sgc.disco_rms_norm_bwd(h, w, gy, gh=gh, axis=axis, eps=EPS)
+        H, G = h.double(), gy.double() * per(w.double(), h, axis)
+        rstd = (H.square().mean(axis, keepdim=True) + EPS).rsqrt()
+        mean, size = (G * H).mean(axis, keepdim=True), (G * H).abs().mean(axis, keepdim=True)
+        a, b, c = rstd * G, H * rstd ** 3 * mean, gh.double() if with_gh else torch.zeros_like(H)
+        ref = a - b + c
+        # rstd 42 u and two products; rstd^3 126 u and four products, the mean's own 82 u of its terms' sizes; two sums
+        bound = U * (46 * a.abs() + 134 * b.abs() + 84 * H.abs() * rstd ** 3 * size + 3 * (a.abs() + b.abs() + c.abs()))
+        close(gx, ref, ref.abs() * half(dt) * 1.001 + bound + floor_of(dt), "gx")
+        terms = gy.double() * H * rstd
+        dims = [i for i in range(h.dim()) if i != axis % h.dim()]
+        rdw, sdw = (terms.sum(dims), terms.abs().sum(dims)) if dims else (terms, terms.abs())
+        # each term 44 u; chains of at most 200 additions in fp32, then fp64
+        close(dw, rdw, rdw.abs() * half(wdt) * 1.001 + 244 * U * sdw + floor_of(wdt), "dw")
+
+
+def test_norm_bwd_against_differences():
+    # the directional derivative of <gy, y> + <gh, h> in x and in w, by central differences in fp64 of the formula
+    shape = (2, 24, 9, 15)
+    h, gy, gh = (randn(shape, torch.float32, s) for s in (31, 32, 33))
+    w = randn((24,), torch.float32, 34)
+    gx, dw = sgc.disco_rms_norm_bwd(h, w, gy, gh=gh, axis=1, eps=EPS)
+
+    def loss(h, w):
+        y = h * (h.square().mean(1, keepdim=True) + EPS).rsqrt() * per(w, h, 1)
+        return float((gy.double() * y).sum() + (gh.double() * h).sum())
+
+    dx, dv = randn(shape, torch.float32, 35).double(), randn((24,), torch.float32, 36).double()
+    s = 2.0 ** -12  # the difference's own error is of the order s^2, 6e-8 of the third derivative
+    fx = (loss(h.double() + s * dx, w.double()) - loss(h.double() - s * dx, w.double())) / (2 * s)
+    fw = (loss(h.double(), w.double() + s * dv) - loss(h.double(), w.double() - s * dv)) / (2 * s)
+    assert abs(float((gx.double() * dx).sum()) - fx) <= 1e-5 * float((gx.double() * dx).abs().sum())
+    assert abs(float((dw.double() * dv).sum()) - fw) <= 1e-5 * float((dw.double() * dv).abs().sum())
+
+
+@pytest.mark.parametrize("case", [((40, 256), -1), ((40, 1000), -1), ((2, 32, 16, 16), 1), ((3, 20000), -1), ((1, 5000, 4, 16), 1), ((9, 24, 3), 1)], ids=ids)
+def test_norm_special_values(case):
+    shape, axis = case
+    dt = torch.bfloat16
+    x = randn(shape, dt, 41)
+    view = x.movedim(axis, -1)  # (..., D): the points in front
+    pts = [tuple(i) for i in torch.cartesian_prod(*[torch.arange(s) for s in view.shape[:-1]]).view(-1, view.dim() - 1).tolist()][:3]
+    view[pts[0]][:] = 0.0
+    view[pts[1]][1] = float("nan")
+    view[pts[2]][2] = float("inf")
+    w = randn((shape[axis],), torch.float32, 42)
+    X = x.double()
+    ref = (X * (X.square().mean(axis, keepdim=True) + EPS).rsqrt() * per(w.double(), x, axis)).movedim(axis, -1)
+    y = sgc.disco_rms_norm(x, w, axis=axis, eps=EPS).movedim(axis, -1)
+    assert bool((y[pts[0]] == 0).all())
+    assert torch.equal(y.isnan(), ref.isnan()) and torch.equal(y.isinf(), ref.isinf())
+    q, scale = sgc.disco_rms_norm_f8(x, w, axis=axis, eps=EPS)
+    qv, sv = q.float().movedim(axis, -1), scale.movedim(axis, -1)
+    assert bool((qv[pts[0]] == 0).all()) and float(sv[pts[0]][0]) == 2.0 ** -126
+    for p in pts[1:]:
+        assert bool(qv[p].isnan().all()) and bool(sv[p].isnan().all())
+    assert int(sv.isnan().sum()) == 2
+    gy = randn(shape, dt, 43)
+    gx, dw = sgc.disco_rms_norm_bwd(x, w, gy, axis=axis, eps=EPS)
+    bad = gx.movedim(axis, -1).isnan().any(-1)
+    assert int(bad.sum()) == 2 and bool(bad[pts[1]]) and bool(bad[pts[2]])
+    assert bool(dw.isnan().any())
+
+
+def test_f8_of_huge_weights():
+    # y beyond fp32's range: infinite scales, as amax / qmax gives them, and quotients of 0 and NaN
+    x = torch.ones((2, 64), device=DEV)
+    w = torch.ones(64, device=DEV)
+    x[0, 5] = 2.0
+    w[5] = 3.0e38
+    q, scale = sgc.disco_rms_norm_f8(x, w, axis=-1, group=32)
+    y = (x * torch.rsqrt(x.square().mean(1, keepdim=True) + EPS) * w).view(2, 2, 32)
+    ref_s = (y.abs().amax(2) / 448.0).clamp(min=2.0 ** -126)
+    assert torch.equal(scale.isinf(), ref_s.isinf()) and torch.equal(scale.isnan(), ref_s.isnan())
+    ref_q = (y / ref_s.unsqueeze(2)).view(2, 64)
+    assert torch.equal(q.float().isnan(), ref_q.isnan())
+    fine = ~ref_q.isnan()
+    assert torch.equal((q.float() == 0)[fine], (ref_q.to(torch.float8_e4m3fn).float() == 0)[fine])
+
+
+def test_every_f8_code_is_read():
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)
+    for qt in (torch.float8_e4m3fn, torch.float8_e5m2):
+        ref = codes.view(qt).float()
+        for shape in ((1, 256), (1, 2, 128)):
+            q = codes.view(shape).to(DEV).view(qt)
+            s = torch.full((1, 1) if len(shape) == 2 else (1, 1, 128), 2.0, device=DEV)
+            out = sgc.disco_dequantize(q, s, dtype=torch.float32, axis=1).cpu().flatten()
+            assert torch.equal(out.isnan(), ref.isnan())
+            assert torch.equal(out[~ref.isnan()], (2 * ref)[~ref.isnan()])
+
+
+def test_norm_empty_and_strided():
+    w = torch.ones(4, device=DEV)
+    x = torch.empty((0, 4, 3), device=DEV)
+    assert sgc.disco_rms_norm(x, w).shape == x.shape
+    gx, dw = sgc.disco_rms_norm_bwd(x, w, x)
+    assert gx.shape == x.shape and bool((dw == 0).all())
+    with pytest.raises(ValueError):
+        sgc.disco_rms_norm(torch.ones((3, 2, 4), device=DEV).movedim(1, 2), w)
+
+
+def test_outputs_may_not_overlap():
+    x = torch.ones((8, 32), device=DEV)
+    w = torch.ones(32, device=DEV)
+    for call in (lambda: sgc.disco_rms_norm(x, w, axis=-1, y=x),
+                 lambda: sgc.disco_rms_norm(x, w, residual=x, axis=-1, h=x),
+                 lambda: sgc.disco_rms_norm_bwd(x, w, x, axis=-1, gx=x),
+                 lambda: sgc.disco_rms_norm_bwd(x, w, x, axis=-1, dw=w),
+                 lambda: sgc.disco_clip_grads([x, w], 1.0, out=[torch.empty_like(x), x.view(-1)[:32]]),
+                 lambda: sgc.disco_clip_grads([x, x], 1.0)):
+        with pytest.raises(sgc.DiscoError) as e:
+            call()
+        assert e.value.status_name == "DISCO_ERR_INVALID_ARGUMENT" and "overlap" in str(e.value)
+    torch.cuda.synchronize()
+    assert bool((x == 1).all()) and bool((w == 1).all())
+
+
+LISTS = [[1], [0], [5, 0, 7], [257] * 9, [1 << 20, 3, 70001, 12], [2048, 2049, 4095, 4097], [17] * 130, [3] * 400, [5000] * 260, [9_000_001]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16", "mixed"])
+@pytest.mark.parametrize("sizes", LISTS, ids=lambda v: f"{len(v)}x{v[0]}")
+def test_grad_norm_and_clip(sizes, dtype):
+    print(f"[clip] {len(sizes)} tensors of {sizes[0]}.. {dtype}", flush=True)
+    flat = {d: randn((sum(sizes) + 1,), T[d], 51, 0.5) for d in T}
+    grads, at = [], 1  # views into flat buffers: no start is aligned
+    for i, n in enumerate(sizes):
+        grads.append(flat[dtype if dtype != "mixed" else ("f32", "bf16", "f16")[i % 3]][at:at + n])
+        at += n
+    ref = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    norm = sgc.disco_grad_norm(grads)
+    assert norm.shape == () and abs(float(norm) - ref) <= 2 * U * ref  # fp64 sums, one rounding
+    for max_norm in (ref / 3 + 1e-3, 1e30):
+        factor = min(1.0, max_norm / (ref + EPS))
+        outs = [torch.full_like(g, float("nan")) for g in grads]
+        n2 = sgc.disco_clip_grads(grads, max_norm, out=outs)
+        assert float(n2) == float(norm)
+        for g, o in zip(grads, outs):
+            r = g.double() * factor
+            close(o, r, r.abs() * (half(g.dtype) + 4 * U) * 1.001 + floor_of(g.dtype), "out")  # the factor 3 u, the product 1
+        mine = [g.clone() for g in grads]
+        sgc.disco_clip_grads(mine, max_norm)
+        assert all(torch.equal(a, b) for a, b in zip(mine, outs))
+
+
+def test_grad_norm_of_none_and_of_extremes():
+    assert float(sgc.disco_grad_norm([])) == 0.0
+    assert float(sgc.disco_clip_grads([], 1.0)) == 0.0
+    big = torch.full((3,), 1e30, device=DEV)  # squares beyond fp32's range
+    assert abs(float(sgc.disco_grad_norm([big])) / (1e30 * math.sqrt(3)) - 1) <= 2 ** -22
+    small = torch.full((4,), 1e-40, device=DEV)  # and below it
+    assert abs(float(sgc.disco_grad_norm([small])) / 2e-40 - 1) <= 2 ** -5  # a subnormal norm has few bits
+    for bad in (float("nan"), float("inf")):
+        g = torch.ones(70000, device=DEV)
+        g[6] = bad
+        n = sgc.disco_clip_grads([g], 1.0)
+        ref = torch.tensor(bad)
+        assert torch.equal(n.cpu().isnan(), ref.isnan()) and torch.equal(n.cpu().isinf(), ref.isinf())
+        assert bool(g.isnan().all()) if bad != bad else (bool(g[6].isnan()) and bool((g[7:] == 0).all()))
+
+
+def test_results_repeat_and_streams():
+    x, gy = randn((2, 96, 40, 51), torch.bfloat16, 61), randn((2, 96, 40, 51), torch.bfloat16, 62)
+    w = randn((96,), torch.float32, 63)
+    first = [*sgc.disco_rms_norm(x, w, residual=gy), *sgc.disco_rms_norm_bwd(x, w, gy, gh=gy),
+             sgc.disco_grad_norm([x, gy])]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            runs.append([*sgc.disco_rms_norm(x, w, residual=gy), *sgc.disco_rms_norm_bwd(x, w, gy, gh=gy),
+                         sgc.disco_grad_norm([x, gy])])
+    torch.cuda.synchronize()
+    for r in runs:
+        assert all(torch.equal(a, b) for a, b in zip(first, r))
+
+
+def test_graph_replays():
+    x, r = randn((2, 80, 20, 33), torch.bfloat16, 71), randn((2, 80, 20, 33), torch.bfloat16, 72)
+    w = randn((80,), torch.float32, 73)
+
+    def step():
+        y, h = sgc.disco_rms_norm(x, w, residual=r)
+        q, s, h2 = sgc.disco_rms_norm_f8(x, w, residual=r, group=32)
+        back = sgc.disco_dequantize(q, s, group=32)
+        gx, dw = sgc.disco_rms_norm_bwd(h, w, y, gh=back)
+        outs = [torch.empty_like(gx), torch.empty_like(dw)]
+        n = sgc.disco_clip_grads([gx, dw], 0.5, out=outs)
+        return [y, h, q.view(torch.uint8), s, back, gx, dw, n, *outs]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for k in range(4):
+        x.copy_(randn(x.shape, torch.bfloat16, 80 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), f"replay {k}"
+
+
+def test_offsets_beyond_32_bits():
+    # 3 x (2^30 + 72) points of bf16: byte offsets pass 2^32 and element offsets 2^31
+    M = (1 << 30) + 72
+    x = torch.empty((1, 3, M), dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(5))
+    w = randn((3,), torch.float32, 91)
+    y = sgc.disco_rms_norm(x, w)
+    q, s = sgc.disco_rms_norm_f8(x, w)
+    back = sgc.disco_dequantize(q, s)
+    gx, dw = sgc.disco_rms_norm_bwd(x, w, x)
+    torch.cuda.synchronize()
+    for lo in (0, M // 2, M - 4096):
+        c = slice(lo, lo + 4096)
+        H = x[..., c].double()
+        rstd = (H.square().mean(1, keepdim=True) + EPS).rsqrt()
+        W = w.double().view(1, 3, 1)
+        ref = H * rstd * W
+        close(y[..., c], ref, ref.abs() * (half(torch.bfloat16) + 46 * U) * 1.001 + 1e-40, "y")
+        top = ref.abs().amax(1, keepdim=True)
+        close(back[..., c], ref, ref.abs() * (2 ** -4 + 2 ** -8) * 1.01 + top / 448 * 2.0 ** -10 * 1.01, "back")
+        a, b = rstd * H * W, H * rstd ** 3 * (H * H * W).mean(1, keepdim=True)
+        size = (H * H * W).abs().mean(1, keepdim=True)
+        bound = U * (49 * a.abs() + 137 * b.abs() + 84 * H.abs() * rstd ** 3 * size)
+        close(gx[..., c], a - b, (a - b).abs() * half(torch.bfloat16) * 1.001 + bound + 1e-40, "gx")
+    del y, q, s, back, gx
+    n = float(sgc.disco_grad_norm([x]))
+    ref = math.sqrt(sum(float(x[0, i, j:j + (1 << 28)].double().square().sum()) for i in range(3) for j in range(0, M, 1 << 28)))
+    assert abs(n - ref) <= 2 * U * ref
