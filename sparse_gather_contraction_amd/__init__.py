@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -305,26 +306,48 @@ def disco_fused_conv_bwd_saved(psi: Psi, out, W, gy, gx=None, dW=None, workspace
 
 # ---- the operators around the convolution in a residual model's training step
 
-_CODES = {}  # torch dtype -> disco_dtype
+# A call on little data is bound by the host, so these wrappers pass each TensorDesc as its packed bytes.
+
+_pack = struct.Struct("Pii5q").pack  # TensorDesc
+_PAD = [(0,) * (5 - n) for n in range(6)]
+_torch = None
+_codes = {}     # torch dtype -> disco_dtype
+_fast = {}      # entry points that take packed descriptors
 
 
-def _codes():
-    if not _CODES:
+def _entry(name):
+    """The library's function `name` with descriptors passed as bytes (or None)."""
+    global _torch
+    f = _fast.get(name)
+    if f is None:
         import torch
 
-        _CODES.update({torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16,
+        _torch = torch
+        _codes.update({torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16,
                        torch.float8_e4m3fn: DISCO_F8_E4M3, torch.float8_e5m2: DISCO_F8_E5M2})
-    return _CODES
+        lib = load_library()
+        f = lib[name]
+        f.argtypes = [ctypes.c_void_p if t is ctypes.POINTER(TensorDesc) else t for t in getattr(lib, name).argtypes]
+        f.restype = ctypes.c_int
+        _fast[name] = f
+    return f
 
 
 def _desc(t):
-    """tensor_desc of a tensor of any of the library's types, or None for None."""
-    if t is None:
-        return None
+    """The packed TensorDesc of a contiguous tensor of any of the library's types."""
     if not t.is_contiguous():
         raise ValueError("disco tensors must be contiguous")
     shape = t.shape
-    return TensorDesc(t.data_ptr(), _codes().get(t.dtype, 99), len(shape), shape[:5])
+    n = len(shape)
+    if n > 5:  # refused by the library
+        shape = shape[:5]
+    return _pack(t.data_ptr(), _codes.get(t.dtype, 99), n, *shape, *_PAD[len(shape)])
+
+
+def _raw_stream(t) -> int:
+    """The current stream of the tensor's device."""
+    i = t.get_device()
+    return _torch._C._cuda_getCurrentRawStream(i) if i >= 0 else 0  # the library refuses host memory
 
 
 def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
@@ -332,15 +355,16 @@ def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
 
     Returns y, or (y, h) with a residual.  axis 1 normalises fields (B, C, H, W) over their channels, -1 rows
     (points, C); w (D,) is fp32 or of x's type."""
-    import torch
-
+    f = _entry("disco_rms_norm")
     if y is None:
-        y = torch.empty_like(x)
-    if residual is not None and h is None:
-        h = torch.empty_like(x)
-    _check(load_library().disco_rms_norm(_desc(x), _desc(residual), _desc(w), axis, eps, _desc(y), _desc(h),
-                                         _stream(x.device)))
-    return y if residual is None else (y, h)
+        y = _torch.empty_like(x)
+    if residual is None:
+        _check(f(_desc(x), None, _desc(w), axis, eps, _desc(y), None if h is None else _desc(h), _raw_stream(x)))
+        return y
+    if h is None:
+        h = _torch.empty_like(x)
+    _check(f(_desc(x), _desc(residual), _desc(w), axis, eps, _desc(y), _desc(h), _raw_stream(x)))
+    return y, h
 
 
 def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None, q=None, scale=None, h=None):
@@ -348,35 +372,34 @@ def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None
 
     q is of `dtype` (torch.float8_e4m3fn, the default, or torch.float8_e5m2); scale (fp32) has x's shape with the axis
     replaced by the number of runs of `group` entries (0: one run, the whole axis; else a multiple of 32)."""
-    import torch
-
+    f = _entry("disco_rms_norm_f8")
     if q is None:
-        q = torch.empty_like(x, dtype=dtype or torch.float8_e4m3fn)
+        q = _torch.empty_like(x, dtype=dtype or _torch.float8_e4m3fn)
     if scale is None:
         shape = list(x.shape)
         shape[axis] = -(-shape[axis] // group) if group > 0 else 1
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scale = _torch.empty(shape, dtype=_torch.float32, device=x.device)
     if residual is not None and h is None:
-        h = torch.empty_like(x)
-    _check(load_library().disco_rms_norm_f8(_desc(x), _desc(residual), _desc(w), axis, eps, group, _desc(q),
-                                            _desc(scale), _desc(h), _stream(x.device)))
+        h = _torch.empty_like(x)
+    _check(f(_desc(x), None if residual is None else _desc(residual), _desc(w), axis, eps, group, _desc(q),
+             _desc(scale), None if h is None else _desc(h), _raw_stream(x)))
     return (q, scale) if residual is None else (q, scale, h)
 
 
 def disco_dequantize(q, scale, dtype=None, axis=1, group=0, out=None):
     """out = q * scale in `dtype` (default bf16): the reader of disco_rms_norm_f8's form."""
-    import torch
-
+    f = _entry("disco_dequantize")
     if out is None:
-        out = torch.empty_like(q, dtype=dtype or torch.bfloat16)
-    _check(load_library().disco_dequantize(_desc(q), _desc(scale), axis, group, _desc(out), _stream(q.device)))
+        out = _torch.empty_like(q, dtype=dtype or _torch.bfloat16)
+    _check(f(_desc(q), _desc(scale), axis, group, _desc(out), _raw_stream(q)))
     return out
 
 
 def disco_rms_norm_bwd_workspace(h, axis=1) -> int:
     """Workspace bytes disco_rms_norm_bwd needs for this h."""
     n = ctypes.c_size_t()
-    _check(load_library().disco_rms_norm_bwd_workspace(_desc(h), axis, ctypes.byref(n)))
+    f = _entry("disco_rms_norm_bwd_workspace")
+    _check(f(_desc(h), axis, n))
     return int(n.value)
 
 
@@ -385,59 +408,54 @@ def disco_rms_norm_bwd(h, w, gy, gh=None, axis=1, eps=1e-6, gx=None, dw=None, wo
 
     gh is the gradient that reaches h past the norm; gx is the gradient of x and of the residual alike.  The
     workspace (a uint8 device tensor) is allocated here when not given."""
-    import torch
-
+    f, g, n = _entry("disco_rms_norm_bwd"), _entry("disco_rms_norm_bwd_workspace"), ctypes.c_size_t()
     if gx is None:
-        gx = torch.empty_like(h)
+        gx = _torch.empty_like(h)
     if dw is None:
-        dw = torch.empty_like(w)
-    lib, d, n = load_library(), _desc(h), ctypes.c_size_t()
-    _check(lib.disco_rms_norm_bwd_workspace(d, axis, n))
+        dw = _torch.empty_like(w)
+    d = _desc(h)
     if workspace is None:
-        workspace = torch.empty(max(n.value, 1), dtype=torch.uint8, device=h.device)
-    _check(lib.disco_rms_norm_bwd(d, _desc(w), _desc(gy), _desc(gh), axis, eps, _desc(gx), _desc(dw),
-                                  workspace.data_ptr(), workspace.numel(), _stream(h.device)))
+        _check(g(d, axis, n))
+        workspace = _torch.empty(n.value or 1, dtype=_torch.uint8, device=h.device)
+    _check(f(d, _desc(w), _desc(gy), None if gh is None else _desc(gh), axis, eps, _desc(gx), _desc(dw),
+             workspace.data_ptr(), workspace.numel(), _raw_stream(h)))
     return gx, dw
 
 
 def _flat_descs(tensors):
     """An array of TensorDesc, each tensor as its elements in a row."""
-    import torch
-
-    if not all(map(torch.Tensor.is_contiguous, tensors)):
+    tensor = _torch.Tensor
+    if not all(map(tensor.is_contiguous, tensors)):
         raise ValueError("disco tensors must be contiguous")
-    a = np.zeros((max(len(tensors), 1), ctypes.sizeof(TensorDesc) // 8), np.int64)
+    a = np.zeros((len(tensors) or 1, 7), np.int64)
     if tensors:
-        a[:, 0] = list(map(torch.Tensor.data_ptr, tensors))
-        codes = _codes()
+        a[:, 0] = list(map(tensor.data_ptr, tensors))
         kinds = {t.dtype for t in tensors}
         if len(kinds) == 1:
-            a[:, 1] = codes.get(kinds.pop(), 99) | 1 << 32
+            a[:, 1] = _codes.get(kinds.pop(), 99) | 1 << 32
         else:
-            a[:, 1] = [codes.get(t.dtype, 99) | 1 << 32 for t in tensors]
-        a[:, 2] = list(map(torch.Tensor.numel, tensors))
+            a[:, 1] = [_codes.get(t.dtype, 99) | 1 << 32 for t in tensors]
+        a[:, 2] = list(map(tensor.numel, tensors))
     return a
 
 
-def _grads(grads, device):
-    import torch
-
-    grads = list(grads)
+def _grad_workspace(grads, device):
+    """(descriptors, norm, workspace) of a call on the list `grads`."""
+    f, n = _entry("disco_grad_norm_workspace"), ctypes.c_size_t()
     if device is None:
-        device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    a, n = _flat_descs(grads), ctypes.c_size_t()
-    _check(load_library().disco_grad_norm_workspace(len(grads), a.ctypes.data, n))
-    norm = torch.empty((), dtype=torch.float32, device=device)
-    return grads, a, norm, torch.empty(n.value, dtype=torch.uint8, device=device), device
+        device = grads[0].device if grads else _torch.device("cuda", _torch.cuda.current_device())
+    a = _flat_descs(grads)
+    _check(f(len(grads), a.ctypes.data, n))
+    return a, _torch.empty((), dtype=_torch.float32, device=device), _torch.empty(n.value, dtype=_torch.uint8, device=device)
 
 
 def disco_grad_norm(grads, device=None):
     """The norm over all elements of all tensors of the list `grads`, as a 0-dimensional fp32 tensor on their device.
 
     The tensors may differ in shape and type (fp32, bf16, fp16); squares are summed in fp64."""
-    grads, a, norm, ws, device = _grads(grads, device)
-    _check(load_library().disco_grad_norm(len(grads), a.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(),
-                                          _stream(device)))
+    f, grads = _entry("disco_grad_norm"), list(grads)
+    a, norm, ws = _grad_workspace(grads, device)
+    _check(f(len(grads), a.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(), _raw_stream(norm)))
     return norm
 
 
@@ -445,14 +463,14 @@ def disco_clip_grads(grads, max_norm, out=None, eps=1e-6, device=None):
     """Scale all gradients by min(1, max_norm / (norm + eps)), norm = disco_grad_norm(grads); returns that norm.
 
     In place, or into the tensors of the list `out`.  The factor never leaves the device."""
-    grads, a, norm, ws, device = _grads(grads, device)
-    if out is None:
-        o = a
-    else:
+    f, grads = _entry("disco_clip_grads"), list(grads)
+    a, norm, ws = _grad_workspace(grads, device)
+    o = a
+    if out is not None:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have one tensor for each gradient")
         o = _flat_descs(out)
-    _check(load_library().disco_clip_grads(len(grads), a.ctypes.data, max_norm, eps, o.ctypes.data, _desc(norm),
-                                           ws.data_ptr(), ws.numel(), _stream(device)))
+    _check(f(len(grads), a.ctypes.data, max_norm, eps, o.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(),
+             _raw_stream(norm)))
     return norm

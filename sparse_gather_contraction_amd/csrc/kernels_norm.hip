@@ -29,7 +29,7 @@ struct NormArgs {
 
 // A workgroup: 2^lg lanes along the points, `groups` threads along the channels, `CPT` channels a thread.
 // LDS: [parts][P] partial sums (a part: a wave, or the threads of one g where those are more), [P] rstd, and for 8-bit outputs [ngroups][P] maxima.
-template <typename T, int VEC, int CPT, bool RES, bool F8>
+template <typename T, int VEC, int CPT, bool RES, bool F8, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
 {
     extern __shared__ float lds[];
@@ -37,7 +37,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
     const int P = VEC << a.lg, in_wave = a.lg < 6 ? 6 : a.lg, parts = blockDim.x >> in_wave, part = t >> in_wave;
     float *sums = lds, *rs = lds + parts * P;
     uint32_t *mx = (uint32_t *)(rs + P);
-    const ColPos pos = col_pos(blockIdx.x, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
+    const int64_t tile = NT ? blockIdx.x : xcd_tile(blockIdx.x, gridDim.x);
+    const ColPos pos = col_pos(tile, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
     const int c0 = g * CPT;
     const int64_t base = pos.n * a.D * a.M + pos.m;
     const T *x = (const T *)a.x + base, *r = (const T *)a.r + base;
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
         T *hs = (T *)a.h + base;
 #pragma unroll
         for (int j = 0; j < CPT; ++j)
-            if (c0 + j < a.D) store_f32<T, VEC>(hs + (int64_t)(c0 + j) * a.M, h[j]);
+            if (c0 + j < a.D) store_f32<T, VEC, NT>(hs + (int64_t)(c0 + j) * a.M, h[j]);
     }
     __syncthreads();
     for (int p = t; p < P; p += blockDim.x) {
@@ -105,33 +106,29 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
         T *y = (T *)a.y + base;
 #pragma unroll
         for (int j = 0; j < CPT; ++j)
-            if (c0 + j < a.D) store_f32<T, VEC>(y + (int64_t)(c0 + j) * a.M, h[j]);
+            if (c0 + j < a.D) store_f32<T, VEC, NT>(y + (int64_t)(c0 + j) * a.M, h[j]);
     } else {
         // a thread's channels share one scale: CPT divides 32, and 32 divides the group
         const int k = c0 < a.D ? c0 / a.group : 0;
-        uint32_t m[VEC];
+        float m[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) m[e] = 0;
+        for (int e = 0; e < VEC; ++e) m[e] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < CPT; ++j)
-            if (c0 + j < a.D)
+        for (int j = 0; j < CPT; j += 2)  // an odd last channel is taken twice
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const uint32_t b = abs_bits(h[j][e]);
-                    m[e] = m[e] > b ? m[e] : b;
-                }
+            for (int e = 0; e < VEC; ++e)
+                if (c0 + j < a.D) m[e] = max_abs(m[e], h[j][e], h[j + 1 < CPT && c0 + j + 1 < a.D ? j + 1 : j][e]);
         if (c0 < a.D)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) atomicMax(&mx[k * P + lane * VEC + e], m[e]);
+            for (int e = 0; e < VEC; ++e) atomicMax(&mx[k * P + lane * VEC + e], abs_bits(m[e]));
         __syncthreads();
         if (c0 >= a.D) return;
-        float s[VEC], inv[VEC];
-        bool odd = false;  // a scale that is infinite or NaN
+        float s[VEC], mul[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            s[e] = f8_scale(__uint_as_float(mx[k * P + lane * VEC + e]), a.qmax);
-            inv[e] = 1.0f / s[e];
-            odd |= !(s[e] < INFINITY);
+            const F8Scale f = f8_scale(__uint_as_float(mx[k * P + lane * VEC + e]), a.qmax);
+            s[e] = f.scale;
+            mul[e] = f.mul;
         }
         if (c0 == k * a.group) store_f32<float, VEC>(a.scale + (pos.n * a.ngroups + k) * a.M + pos.m, s);
         uint8_t *q = (uint8_t *)a.y + base;
@@ -140,10 +137,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
             if (c0 + j < a.D) {
                 float v[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = odd ? h[j][e] / s[e] : f8_quot(h[j][e], s[e], inv[e]);
+                for (int e = 0; e < VEC; ++e) v[e] = h[j][e] * mul[e];
                 Pack<uint8_t, VEC> pq;
                 pack_f8(v, a.f8, pq);
-                store_pack<uint8_t, VEC>(q + (int64_t)(c0 + j) * a.M, pq);
+                store_pack<uint8_t, VEC, NT>(q + (int64_t)(c0 + j) * a.M, pq);
             }
     }
 }
@@ -170,18 +167,44 @@ __device__ __forceinline__ V row_join(V v, int lg, V *slots, Op op)
 struct AddOp {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
-struct MaxOp {
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+struct MaxOp {  // of values that are 0 or more; a NaN is kept
+    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
 };
+
+// Zeroes what the thread holds beside another one, so that it adds nothing to a sum or a maximum.
+template <int VEC>
+__device__ __forceinline__ void drop_dup(float (&h)[VEC], int dup)
+{
+    if (dup)  // only the last vectors of a row
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = e < dup ? 0.0f : h[e];
+}
+
+// Stores the elements of a vector that no other thread holds.
+template <typename T, int VEC, bool NT>
+__device__ __forceinline__ void store_own(T *p, const Pack<T, VEC> &r, int dup)
+{
+    if (dup == 0) {
+        store_pack<T, VEC, NT>(p, r);
+    } else {
+        const uint32_t per = 4 / sizeof(T);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (e >= dup) {
+                if constexpr (sizeof(T) == 4) ((uint32_t *)p)[e] = r.w[e];
+                else if constexpr (sizeof(T) == 2) ((uint16_t *)p)[e] = (uint16_t)(r.w[e / per] >> (16 * (e % per)));
+                else ((uint8_t *)p)[e] = (uint8_t)(r.w[e / per] >> (8 * (e % per)));
+            }
+    }
+}
 
 // 2^lg threads a row, KPT vectors a thread.  Dynamic LDS: 8-bit outputs with groups that no run of lanes
 // can join keep [rows][ngroups] maxima there.
-template <typename T, int VEC, int KPT, bool RES, bool F8>
+template <typename T, int VEC, int KPT, bool RES, bool F8, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
 {
     extern __shared__ uint32_t mx[];
-    __shared__ float fslots[kNormMaxThreads / 64];
-    __shared__ uint32_t uslots[kNormMaxThreads / 64];
+    __shared__ float slots[kNormMaxThreads / 64];
     const int t = threadIdx.x, lanes = 1 << a.lg, tt = t & (lanes - 1), slot = t >> a.lg;
     const int64_t want = (int64_t)blockIdx.x * (blockDim.x >> a.lg) + slot;
     const int64_t row = want < a.N ? want : a.N - 1;  // a slot past the end repeats the last row
@@ -205,20 +228,24 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) h[k][e] += f[e];
             }
+            drop_dup(h[k], pos[k].dup);
         }
     }
     float ss = 0.0f;
 #pragma unroll
     for (int k = 0; k < KPT; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss = e >= pos[k].dup ? __builtin_fmaf(h[k][e], h[k][e], ss) : ss;
-    ss = row_join(ss, a.lg, fslots, AddOp());
+        for (int e = 0; e < VEC; ++e) ss = __builtin_fmaf(h[k][e], h[k][e], ss);
+    ss = row_join(ss, a.lg, slots, AddOp());
     const float rstd = rsqrtf(ss / (float)a.D + a.eps);
     if constexpr (RES) {
         T *hs = (T *)a.h + row * a.D;
 #pragma unroll
-        for (int k = 0; k < KPT; ++k)
-            if (pos[k].dup < VEC) store_f32<T, VEC>(hs + pos[k].c, h[k]);
+        for (int k = 0; k < KPT; ++k) {
+            Pack<T, VEC> p;
+            pack(h[k], p);
+            store_own<T, VEC, NT>(hs + pos[k].c, p, pos[k].dup);
+        }
     }
 #pragma unroll
     for (int k = 0; k < KPT; ++k) {
@@ -231,25 +258,26 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
     if constexpr (!F8) {
         T *y = (T *)a.y + row * a.D;
 #pragma unroll
-        for (int k = 0; k < KPT; ++k)
-            if (pos[k].dup < VEC) store_f32<T, VEC>(y + pos[k].c, h[k]);
+        for (int k = 0; k < KPT; ++k) {
+            Pack<T, VEC> p;
+            pack(h[k], p);
+            store_own<T, VEC, NT>(y + pos[k].c, p, pos[k].dup);
+        }
     } else {
-        uint32_t m[KPT];
+        float m[KPT];
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-            m[k] = 0;
+            drop_dup(h[k], pos[k].dup);  // a NaN rstd or weight has come back into the zeroes
+            m[k] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const uint32_t b = abs_bits(h[k][e]);
-                m[k] = e >= pos[k].dup && b > m[k] ? b : m[k];
-            }
+            for (int e = 0; e < VEC; e += 2) m[k] = max_abs(m[k], h[k][e], h[k][e + 1 < VEC ? e + 1 : e]);
         }
         const int gv = a.group / VEC;  // vectors of a group
         if (a.ngroups == 1) {
-            uint32_t all = m[0];
+            float all = m[0];
 #pragma unroll
-            for (int k = 1; k < KPT; ++k) all = all > m[k] ? all : m[k];
-            all = row_join(all, a.lg, uslots, MaxOp());
+            for (int k = 1; k < KPT; ++k) all = MaxOp()(all, m[k]);
+            all = row_join(all, a.lg, slots, MaxOp());
 #pragma unroll
             for (int k = 0; k < KPT; ++k) m[k] = all;
         } else if ((gv & (gv - 1)) == 0 && gv <= (lanes < 64 ? lanes : 64)) {
@@ -262,32 +290,25 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < KPT; ++k)
-                if (pos[k].dup < VEC) atomicMax(&mine[((k * lanes + tt) * VEC) / a.group], m[k]);
+                if (pos[k].dup < VEC) atomicMax(&mine[((k * lanes + tt) * VEC) / a.group], abs_bits(m[k]));
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < KPT; ++k)
-                if (pos[k].dup < VEC) m[k] = mine[((k * lanes + tt) * VEC) / a.group];
+                if (pos[k].dup < VEC) m[k] = __uint_as_float(mine[((k * lanes + tt) * VEC) / a.group]);
         }
         uint8_t *q = (uint8_t *)a.y + row * a.D;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             if (pos[k].dup >= VEC) continue;
-            const int c = (k * lanes + tt) * VEC, grp = c / a.group;
-            const float s = f8_scale(__uint_as_float(m[k]), a.qmax), inv = 1.0f / s;
-            const bool odd = !(s < INFINITY);
-            if (c == grp * a.group) a.scale[row * a.ngroups + grp] = s;
+            const int c = (k * lanes + tt) * VEC, grp = a.ngroups == 1 ? 0 : c / a.group;
+            const F8Scale f = f8_scale(m[k], a.qmax);
+            if (c == grp * a.group) a.scale[row * a.ngroups + grp] = f.scale;
             float v[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = odd ? h[k][e] / s : f8_quot(h[k][e], s, inv);
+            for (int e = 0; e < VEC; ++e) v[e] = h[k][e] * f.mul;
             Pack<uint8_t, VEC> pq;
             pack_f8(v, a.f8, pq);
-            if (pos[k].dup == 0) {
-                store_pack<uint8_t, VEC>(q + pos[k].c, pq);
-            } else {  // the elements held twice may belong to another group's scale
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (e >= pos[k].dup) q[pos[k].c + e] = (uint8_t)(pq.w[e / 4] >> (8 * (e & 3)));
-            }
+            store_own<uint8_t, VEC, NT>(q + pos[k].c, pq, pos[k].dup);
         }
     }
 }
@@ -332,12 +353,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_loop_kernel(NormArgs a)
             store_elem((T *)a.y + base, (int64_t)c * a.M, v * rstd * load_weight<T>(a.w, a.wf32, c));
         }
     } else {
-        uint32_t *mx = (uint32_t *)sums;  // [groups][P]: the group's maximum over the threads
+        float *mx = sums;  // [groups][P]: the group's maximum over the threads
         for (int k = 0; k < a.ngroups; ++k) {
             const int lo = k * a.group, hi = lo + a.group < a.D ? lo + a.group : a.D;
-            uint32_t m = 0;
-            for (int c = lo + g; c < hi; c += groups)
-                m = MaxOp()(m, abs_bits(value(c) * rstd * load_weight<T>(a.w, a.wf32, c)));
+            float m = 0.0f;
+            for (int c = lo + g; c < hi; c += groups) {
+                const float y = value(c) * rstd * load_weight<T>(a.w, a.wf32, c);
+                m = max_abs(m, y, y);
+            }
             __syncthreads();
             mx[g * P + lane] = m;
             __syncthreads();
@@ -345,14 +368,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_loop_kernel(NormArgs a)
                 if (g < o) mx[g * P + lane] = MaxOp()(mx[g * P + lane], mx[(g + o) * P + lane]);
                 __syncthreads();
             }
-            const float s = f8_scale(__uint_as_float(mx[lane]), a.qmax), inv = 1.0f / s;
-            const bool odd = !(s < INFINITY);
-            if (g == 0) a.scale[(pos.n * a.ngroups + k) * a.M + pos.m] = s;
+            const F8Scale f = f8_scale(mx[lane], a.qmax);
+            if (g == 0) a.scale[(pos.n * a.ngroups + k) * a.M + pos.m] = f.scale;
             for (int c = lo + g; c < hi; c += groups) {
                 const float v = value(c);
                 if constexpr (RES) store_elem((T *)a.h + base, (int64_t)c * a.M, v);
-                const float y = v * rstd * load_weight<T>(a.w, a.wf32, c);
-                const float q1[1] = {odd ? y / s : f8_quot(y, s, inv)};
+                const float q1[1] = {v * rstd * load_weight<T>(a.w, a.wf32, c) * f.mul};
                 Pack<uint8_t, 1> pq;
                 pack_f8(q1, a.f8, pq);
                 store_pack<uint8_t, 1>((uint8_t *)a.y + base + (int64_t)c * a.M, pq);
@@ -361,33 +382,48 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_loop_kernel(NormArgs a)
     }
 }
 
-template <typename T, bool RES, bool F8>
-hipError_t launch_t(const NormArgs &a, const NormGeom &g, hipStream_t s)
+template <typename T, bool RES, bool F8, bool NT>
+void launch_nt(const NormArgs &a, const NormGeom &g, size_t lds, hipStream_t s)
 {
     constexpr int V = 16 / (int)sizeof(T);
     const dim3 grid((uint32_t)g.tiles), block(g.threads);
-    const size_t lds = norm_lds(g, F8 ? a.ngroups : 0);
-#define ROWS(VEC, KPT) norm_rows_kernel<T, VEC, KPT, RES, F8><<<grid, block, lds, s>>>(a)
-#define COLS(VEC, CPT) norm_cols_kernel<T, VEC, CPT, RES, F8><<<grid, block, lds, s>>>(a)
-    if (g.loop) {
-        norm_loop_kernel<T, RES, F8><<<grid, block, lds, s>>>(a);
-    } else if (g.rows) {
-        if (g.vec == 1) ROWS(1, 1);
-        else if (g.per == 1) ROWS(V, 1);
-        else if (g.per == 2) ROWS(V, 2);
-        else ROWS(V, 4);
-    } else if (g.vec == 1) {
-        if (g.per == 1) COLS(1, 1);
-        else if (g.per == 2) COLS(1, 2);
-        else if (g.per == 4) COLS(1, 4);
-        else COLS(1, 8);
+#define ROWS(KPT) norm_rows_kernel<T, V, KPT, RES, F8, NT><<<grid, block, lds, s>>>(a)
+#define COLS(CPT) norm_cols_kernel<T, V, CPT, RES, F8, NT><<<grid, block, lds, s>>>(a)
+    if (g.rows) {
+        if (g.per == 1) ROWS(1);
+        else if (g.per == 2) ROWS(2);
+        else ROWS(4);
     } else {
-        if (g.per == 1) COLS(V, 1);
-        else if (g.per == 2) COLS(V, 2);
-        else if (g.per == 4) COLS(V, 4);
-        else COLS(V, 8);
+        if (g.per == 1) COLS(1);
+        else if (g.per == 2) COLS(2);
+        else if (g.per == 4) COLS(4);
+        else COLS(8);
     }
 #undef ROWS
+#undef COLS
+}
+
+template <typename T, bool RES, bool F8>
+hipError_t launch_t(const NormArgs &a, const NormGeom &g, hipStream_t s)
+{
+    const dim3 grid((uint32_t)g.tiles), block(g.threads);
+    const size_t lds = norm_lds(g, F8 ? a.ngroups : 0);
+    // Outputs that the last-level cache cannot hold until they are read are stored past it.
+    const int64_t out = a.N * a.D * a.M * ((RES ? sizeof(T) : 0) + (F8 ? 1 : sizeof(T)));
+#define COLS(CPT) norm_cols_kernel<T, 1, CPT, RES, F8, false><<<grid, block, lds, s>>>(a)
+    if (g.loop) {
+        norm_loop_kernel<T, RES, F8><<<grid, block, lds, s>>>(a);
+    } else if (g.vec > 1) {
+        if (out > kStreamBytes) launch_nt<T, RES, F8, true>(a, g, lds, s);
+        else launch_nt<T, RES, F8, false>(a, g, lds, s);
+    } else if (g.rows) {
+        norm_rows_kernel<T, 1, 1, RES, F8, false><<<grid, block, lds, s>>>(a);
+    } else {
+        if (g.per == 1) COLS(1);
+        else if (g.per == 2) COLS(2);
+        else if (g.per == 4) COLS(4);
+        else COLS(8);
+    }
 #undef COLS
     return hipGetLastError();
 }
@@ -428,7 +464,7 @@ struct DequantArgs {
 };
 
 // columns: a thread holds VEC points of CPT channels under one scale.
-template <typename T, int VEC, int CPT>
+template <typename T, int VEC, int CPT, bool NT>
 __global__ __launch_bounds__(256) void dequant_cols_kernel(DequantArgs a)
 {
     const int lane = threadIdx.x & ((1 << a.lg) - 1), g = threadIdx.x >> a.lg;
@@ -453,12 +489,12 @@ __global__ __launch_bounds__(256) void dequant_cols_kernel(DequantArgs a)
             unpack_f8(pq[j], a.f8, v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[e] *= s[e];
-            store_f32<T, VEC>(out + (int64_t)(c0 + j) * a.M, v);
+            store_f32<T, VEC, NT>(out + (int64_t)(c0 + j) * a.M, v);
         }
 }
 
 // rows: 2^lg threads a row, each walking its vectors.
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT>
 __global__ __launch_bounds__(256) void dequant_rows_kernel(DequantArgs a)
 {
     const int lanes = 1 << a.lg, tt = threadIdx.x & (lanes - 1), slot = threadIdx.x >> a.lg;
@@ -474,13 +510,9 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(DequantArgs a)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f[e] *= s;
         T *out = (T *)a.out + row * a.D + pos.c;
-        if (pos.dup == 0) {
-            store_f32<T, VEC>(out, f);
-        } else {  // the elements held twice may belong to another group's scale
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (e >= pos.dup) store_elem(out, e, f[e]);
-        }
+        Pack<T, VEC> p;
+        pack(f, p);
+        store_own<T, VEC, NT>(out, p, pos.dup);  // what is held twice may belong to another group's scale
     }
 }
 
@@ -489,12 +521,15 @@ hipError_t launch_dequant_t(DequantArgs a, const DequantGeom &g, hipStream_t s)
 {
     constexpr int V = 16 / (int)sizeof(T);
     const dim3 grid((uint32_t)g.blocks);
+    const bool nt = a.N * a.D * a.M * (int64_t)sizeof(T) > kStreamBytes;
     if (a.M == 1) {
-        if (g.vec) dequant_rows_kernel<T, V><<<grid, 256, 0, s>>>(a);
-        else dequant_rows_kernel<T, 1><<<grid, 256, 0, s>>>(a);
+        if (!g.vec) dequant_rows_kernel<T, 1, false><<<grid, 256, 0, s>>>(a);
+        else if (nt) dequant_rows_kernel<T, V, true><<<grid, 256, 0, s>>>(a);
+        else dequant_rows_kernel<T, V, false><<<grid, 256, 0, s>>>(a);
     } else {
-        if (g.vec) dequant_cols_kernel<T, V, kDequantCpt><<<grid, 256, 0, s>>>(a);
-        else dequant_cols_kernel<T, 1, kDequantCpt><<<grid, 256, 0, s>>>(a);
+        if (!g.vec) dequant_cols_kernel<T, 1, kDequantCpt, false><<<grid, 256, 0, s>>>(a);
+        else if (nt) dequant_cols_kernel<T, V, kDequantCpt, true><<<grid, 256, 0, s>>>(a);
+        else dequant_cols_kernel<T, V, kDequantCpt, false><<<grid, 256, 0, s>>>(a);
     }
     return hipGetLastError();
 }

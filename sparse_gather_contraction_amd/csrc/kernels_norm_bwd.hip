@@ -27,7 +27,7 @@ struct BwdArgs {
 
 // Columns (M > 1): the forward's tiles.  LDS: [parts][P] sums of h^2, [parts][P] of g h, [P] rstd,
 // [P] rstd^3 mean(g h); at the end [waves of one g][channels] of dw.
-template <typename T, int VEC, int CPT, bool RES>
+template <typename T, int VEC, int CPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 {
     extern __shared__ float lds[];
@@ -42,7 +42,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
         w[j] = c0 + j < a.D ? load_weight<T>(a.w, a.wf32, c0 + j) : 0.0f;
         acc[j] = 0.0f;
     }
-    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    for (int64_t i = blockIdx.x; i < a.tiles; i += gridDim.x) {
+        const int64_t tile = NT ? i : xcd_tile(i, a.tiles);
         const ColPos pos = col_pos(tile, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
         const int64_t base = pos.n * a.D * a.M + pos.m;
         Pack<T, VEC> ph[CPT], pg[CPT], pr[CPT];
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) o[e] += r[e];
             }
-            store_f32<T, VEC>((T *)a.gx + base + (int64_t)(c0 + j) * a.M, o);
+            store_f32<T, VEC, NT>((T *)a.gx + base + (int64_t)(c0 + j) * a.M, o);
         }
     }
     const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
@@ -171,7 +172,7 @@ __device__ __forceinline__ Sum2 row_sum2(Sum2 s, int lg, Sum2 *slots)
 }
 
 // Rows (M = 1).  Dynamic LDS: [rows][D] for the join of dw where a workgroup holds several rows.
-template <typename T, int VEC, int KPT, bool RES>
+template <typename T, int VEC, int KPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 {
     extern __shared__ float lds[];
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) o[e] += r[e];
             }
-            store_f32<T, VEC>((T *)a.gx + base + pos[k].c, o);
+            store_f32<T, VEC, NT>((T *)a.gx + base + pos[k].c, o);
         }
     }
     float *mine = a.partial + (int64_t)blockIdx.x * a.D;
@@ -326,31 +327,45 @@ __global__ __launch_bounds__(1024) void dw_sum_kernel(const float *partial, int 
     if (r0 == 0 && c < D) store_elem(dw, c, (float)part[0][col]);
 }
 
-template <typename T, bool RES>
-hipError_t launch_t(const BwdArgs &a, const NormGeom &g, int blocks, hipStream_t s)
+template <typename T, bool RES, bool NT>
+void launch_nt(const BwdArgs &a, const NormGeom &g, int blocks, size_t lds, hipStream_t s)
 {
     constexpr int V = 16 / (int)sizeof(T);
     const dim3 grid(blocks), block(g.threads);
-    const size_t lds = norm_bwd_lds(g, a.D);
-#define ROWS(VEC, KPT) bwd_rows_kernel<T, VEC, KPT, RES><<<grid, block, lds, s>>>(a)
-#define COLS(VEC, CPT) bwd_cols_kernel<T, VEC, CPT, RES><<<grid, block, lds, s>>>(a)
-    if (g.loop) {
-        bwd_loop_kernel<T, RES><<<grid, block, lds, s>>>(a);
-    } else if (g.rows) {
-        if (g.vec == 1) ROWS(1, 1);
-        else if (g.per == 1) ROWS(V, 1);
-        else if (g.per == 2) ROWS(V, 2);
-        else ROWS(V, 4);
-    } else if (g.vec == 1) {
-        if (g.per == 1) COLS(1, 1);
-        else if (g.per == 2) COLS(1, 2);
-        else COLS(1, 4);
+#define ROWS(KPT) bwd_rows_kernel<T, V, KPT, RES, NT><<<grid, block, lds, s>>>(a)
+#define COLS(CPT) bwd_cols_kernel<T, V, CPT, RES, NT><<<grid, block, lds, s>>>(a)
+    if (g.rows) {
+        if (g.per == 1) ROWS(1);
+        else if (g.per == 2) ROWS(2);
+        else ROWS(4);
     } else {
-        if (g.per == 1) COLS(V, 1);
-        else if (g.per == 2) COLS(V, 2);
-        else COLS(V, 4);
+        if (g.per == 1) COLS(1);
+        else if (g.per == 2) COLS(2);
+        else COLS(4);
     }
 #undef ROWS
+#undef COLS
+}
+
+template <typename T, bool RES>
+hipError_t launch_t(const BwdArgs &a, const NormGeom &g, int blocks, hipStream_t s)
+{
+    const dim3 grid(blocks), block(g.threads);
+    const size_t lds = norm_bwd_lds(g, a.D);
+    const bool nt = a.N * a.D * a.M * (int64_t)sizeof(T) > kStreamBytes;
+#define COLS(CPT) bwd_cols_kernel<T, 1, CPT, RES, false><<<grid, block, lds, s>>>(a)
+    if (g.loop) {
+        bwd_loop_kernel<T, RES><<<grid, block, lds, s>>>(a);
+    } else if (g.vec > 1) {
+        if (nt) launch_nt<T, RES, true>(a, g, blocks, lds, s);
+        else launch_nt<T, RES, false>(a, g, blocks, lds, s);
+    } else if (g.rows) {
+        bwd_rows_kernel<T, 1, 1, RES, false><<<grid, block, lds, s>>>(a);
+    } else {
+        if (g.per == 1) COLS(1);
+        else if (g.per == 2) COLS(2);
+        else COLS(4);
+    }
 #undef COLS
     return hipGetLastError();
 }

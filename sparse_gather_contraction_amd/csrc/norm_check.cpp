@@ -103,8 +103,20 @@ static void check_dequant(int64_t N, int64_t D, int64_t M, int esz)
     for (int h : held) REQUIRE(h == 1);
 }
 
+static void check_xcd()
+{
+    for (int64_t n = 1; n < 400; ++n) {
+        std::vector<int> taken((size_t)n, 0);
+        for (int64_t i = 0; i < n; ++i) {
+            const int64_t t = xcd_tile(i, n);
+            if (t < 0 || t >= n || taken[(size_t)t]++) fail("a tile is taken twice or outside", i, n, t, 0);
+        }
+    }
+}
+
 int main()
 {
+    check_xcd();
     const int64_t Ds[] = {1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 31, 32, 33, 63, 64, 73, 80, 127, 128, 255, 256, 257, 260, 511, 512, 513,
                           1000, 1024, 1025, 2047, 2048, 2049, 4096, 8191, 8192, 16383, 16384, 16385, 32768, 32769, 70001};
     const int64_t Ms[] = {1, 2, 3, 7, 8, 15, 63, 64, 65, 127, 128, 129, 255, 1000, 1303};

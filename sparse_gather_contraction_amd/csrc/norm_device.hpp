@@ -46,7 +46,19 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
     return r;
 }
 
-template <typename T, int VEC>
+// A store that the caches keep, or (NT) one that passes through them.
+template <bool NT, typename V, typename T>
+__device__ __forceinline__ void store_as(T *p, const V &v)
+{
+    if constexpr (NT) {
+        typedef V VU __attribute__((aligned(1)));
+        __builtin_nontemporal_store(v, (VU *)p);
+    } else {
+        __builtin_memcpy(p, &v, sizeof(V));
+    }
+}
+
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &r)
 {
     constexpr int B = Pack<T, VEC>::kBytes;
@@ -54,13 +66,13 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &r)
 #pragma unroll
         for (int i = 0; i < B / 16; ++i) {
             const u32x4 v = {r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]};
-            __builtin_memcpy(p + i * (16 / (int)sizeof(T)), &v, 16);
+            store_as<NT>(p + i * (16 / (int)sizeof(T)), v);
         }
     } else if constexpr (B == 8) {
         const u32x2 v = {r.w[0], r.w[1]};
-        __builtin_memcpy(p, &v, 8);
+        store_as<NT>(p, v);
     } else if constexpr (B == 4) {
-        __builtin_memcpy(p, &r.w[0], 4);
+        store_as<NT>(p, r.w[0]);
     } else if constexpr (B == 2) {
         *(uint16_t *)p = (uint16_t)r.w[0];
     } else {
@@ -145,12 +157,12 @@ __device__ __forceinline__ void load_f32(const T *p, float (&f)[VEC])
     unpack(load_pack<T, VEC>(p), f);
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_f32(T *p, const float (&f)[VEC])
 {
     Pack<T, VEC> r;
     pack(f, r);
-    store_pack<T, VEC>(p, r);
+    store_pack<T, VEC, NT>(p, r);
 }
 
 // 8-bit values (fmt 0: e4m3, 1: e5m2, both with the OCP encodings gfx950 converts to), round to nearest even
@@ -203,25 +215,29 @@ __device__ __forceinline__ float load_weight(const void *w, int wf32, int64_t c)
     return wf32 ? ((const float *)w)[c] : load_elem((const T *)w, c);
 }
 
-// |v| as an unsigned whole number: ordered like the values, with infinity and then NaN above them, so that
-// a maximum over it keeps a NaN.
+// |v| as an unsigned whole number: ordered like the values, with infinity and then NaN above them
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// scale of a group whose largest |y| is amax: amax / qmax, at least 2^-126 (the reciprocal of a smaller one
-// leaves fp32's range); a NaN stays one
-__device__ __forceinline__ float f8_scale(float amax, float qmax)
+// max(m, |a|, |b|), a NaN kept
+__device__ __forceinline__ float max_abs(float m, float a, float b)
 {
-    const float s = amax / qmax;
-    return s < 0x1p-126f ? 0x1p-126f : s;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
-// y / scale rounded once: the product with the reciprocal, corrected by its residual.  An infinite or NaN
-// scale takes the division itself (0 * inf would turn a quotient of 0 into NaN).
-__device__ __forceinline__ float f8_quot(float y, float scale, float inv)
+// The scale of a group whose largest |y| is amax (0 or more), and the factor that takes y to its quotient.
+//   scale = amax / qmax, at least 2^-126 (the reciprocal of a smaller one leaves fp32's range); mul = qmax / amax,
+// which is 1 / scale without scale's own rounding, so y mul is off by one rounding each of the quotient and the
+// product, as y / scale is.  amax infinite: scale infinite and mul 0, so a finite y gives 0 and an infinite one
+// NaN; amax NaN: both NaN.
+struct F8Scale {
+    float scale, mul;
+};
+
+__device__ __forceinline__ F8Scale f8_scale(float amax, float qmax)
 {
-    const float q = y * inv;
-    const float e = __builtin_fmaf(-q, scale, y);
-    return __builtin_fmaf(e, inv, q);
+    const float s = amax / qmax;
+    if (s < 0x1p-126f) return {0x1p-126f, 0x1p126f};
+    return {s, qmax / amax};
 }
 
 }  // namespace disco

@@ -60,6 +60,14 @@ DISCO_HD ColPos col_pos(int64_t tile, int lane, int vec, int lg, int32_t tiles_n
     return p;
 }
 
+// The tile that workgroup i of n takes so that neighbouring tiles go to one XCD (workgroups go round the 8
+// XCDs): the cache lines that two tiles share are then written through one L2.
+DISCO_HD int64_t xcd_tile(int64_t i, int64_t n)
+{
+    const int64_t q = n >> 3, r = n & 7, x = i & 7;
+    return x * q + (x < r ? x : r) + (i >> 3);
+}
+
 // ---- rows
 
 struct RowPos {
@@ -79,6 +87,7 @@ DISCO_HD RowPos row_pos(int v, int vec, int D)
 // ---- geometry
 
 constexpr int kNormMaxThreads = 1024;
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;  // outputs beyond this are stored past the caches
 constexpr int kColsMinM = 64;    // fewer points after the axis than this: flat tiles of single elements
 
 inline int log2_up(int64_t v)
@@ -100,7 +109,7 @@ inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
         if (nv > (int64_t)kNormMaxThreads * 4) {
             g.loop = 1;
         } else {
-            g.per = nv > 512 ? 4 : nv > 32 ? 2 : 1;
+            g.per = nv > (bwd ? 2048 : 512) ? 4 : nv > 32 ? 2 : 1;
             g.lg = log2_up(ceil_div64(nv, g.per));
             const int lanes = 1 << g.lg;
             g.threads = lanes > 256 ? lanes : 256;
@@ -111,11 +120,12 @@ inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
     } else {
         const bool flat = M < kColsMinM;
         g.vec = flat ? 1 : vmax;
-        // channels a thread; lanes along the points: a run of 256 bytes, or fewer where the channels need the threads
-        const int pmax = bwd ? 4 : 8;
-        g.per = D >= pmax * 2 ? pmax : D >= 8 ? 4 : D >= 4 ? 2 : 1;
+        // Channels a thread, then as many lanes along the points as the workgroup has threads for: a run of
+        // 64 lanes x 16 bytes of each channel at most.
+        const int pmax = bwd || D <= 128 ? 4 : 8;
+        g.per = D >= 8 ? pmax : D >= 4 ? 2 : 1;
         const int64_t ng = ceil_div64(D, g.per);
-        int lg = flat ? 6 : 4;
+        int lg = bwd && esz == 2 && !flat ? 5 : 6;  // the backward's LDS holds two sums a point
         while (lg < 8 && (ng << lg) < 256) ++lg;
         while (lg > 2 && (ng << lg) > kNormMaxThreads) --lg;
         if ((ng << lg) > kNormMaxThreads) {
