@@ -74,9 +74,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
         if (c0 + j < a.D)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) ss[e] = __builtin_fmaf(h[j][e], h[j][e], ss[e]);
-    for (int o = 1 << a.lg; o < 64; o <<= 1)  // the wave's threads that hold the same points
+    if (a.lg < 6)  // the wave's threads that hold the same points
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss[e] += __shfl_xor(ss[e], o);
+        for (int e = 0; e < VEC; ++e) ss[e] = join_apart(ss[e], a.lg, AddOp());
     if (a.lg >= 6 || (t & 63) < (1 << a.lg))
 #pragma unroll
         for (int e = 0; e < VEC; ++e) sums[part * P + lane * VEC + e] = ss[e];
@@ -147,12 +147,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
 
 // ---------------------------------------------------------------- rows (M = 1)
 
-// Joins a value over the 2^lg threads of a row: shuffles within a wave, LDS (one slot a wave) beyond it.
-template <typename V, typename Op>
-__device__ __forceinline__ V row_join(V v, int lg, V *slots, Op op)
+// Joins a value over the 2^lg threads of a row: within a wave, then through LDS (one slot a wave).
+template <typename Op>
+__device__ __forceinline__ float row_join(float v, int lg, float *slots, Op op)
 {
-    const int in_wave = lg < 6 ? lg : 6;
-    for (int o = 0; o < in_wave; ++o) v = op(v, __shfl_xor(v, 1 << o));
+    v = join_run(v, lg, op);
     if (lg > 6) {  // uniform over the workgroup
         const int wave = threadIdx.x >> 6, per_row = 1 << (lg - 6), first = wave & ~(per_row - 1);
         __syncthreads();
@@ -163,13 +162,6 @@ __device__ __forceinline__ V row_join(V v, int lg, V *slots, Op op)
     }
     return v;
 }
-
-struct AddOp {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct MaxOp {  // of values that are 0 or more; a NaN is kept
-    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
-};
 
 // Zeroes what the thread holds beside another one, so that it adds nothing to a sum or a maximum.
 template <int VEC>
@@ -281,9 +273,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
 #pragma unroll
             for (int k = 0; k < KPT; ++k) m[k] = all;
         } else if ((gv & (gv - 1)) == 0 && gv <= (lanes < 64 ? lanes : 64)) {
-            for (int o = 1; o < gv; o <<= 1)
+            const int lgv = 31 - __builtin_clz(gv);
 #pragma unroll
-                for (int k = 0; k < KPT; ++k) m[k] = MaxOp()(m[k], __shfl_xor(m[k], o));
+            for (int k = 0; k < KPT; ++k) m[k] = join_run(m[k], lgv, MaxOp());
         } else {
             uint32_t *mine = mx + slot * a.ngroups;
             for (int i = t; i < (int)(blockDim.x >> a.lg) * a.ngroups; i += blockDim.x) mx[i] = 0;

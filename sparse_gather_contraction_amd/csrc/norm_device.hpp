@@ -224,6 +224,60 @@ __device__ __forceinline__ float max_abs(float m, float a, float b)
     return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
+// ---- joins over the lanes of a wave: DPP moves and the row and half swaps, which need no LDS
+
+struct AddOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxOp {  // of values that are 0 or more; a NaN is kept
+    __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// v of the lane's row of 16 and of the row beside it (lane ^ 16), in an order that both rows share
+template <typename Op>
+__device__ __forceinline__ float join16(float v, Op op)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// the same over the wave's halves (lane ^ 32)
+template <typename Op>
+__device__ __forceinline__ float join32(float v, Op op)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Joins v over each run of 2^lg lanes (lg <= 6, uniform), every lane of a run getting the same value.
+template <typename Op>
+__device__ __forceinline__ float join_run(float v, int lg, Op op)
+{
+    if (lg > 0) v = op(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
+    if (lg > 1) v = op(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
+    if (lg > 2) v = op(v, dpp<0x141>(v));  // half mirror: the other quad of the eight, whose lanes agree by now
+    if (lg > 3) v = op(v, dpp<0x140>(v));  // mirror: the other eight of the row
+    if (lg > 4) v = join16(v, op);
+    if (lg > 5) v = join32(v, op);
+    return v;
+}
+
+// Joins v over the lanes of a wave that are 2^lg apart.
+template <typename Op>
+__device__ __forceinline__ float join_apart(float v, int lg, Op op)
+{
+    for (int o = lg; o < 4; ++o) v = op(v, __shfl_xor(v, 1 << o));
+    if (lg < 5) v = join16(v, op);
+    if (lg < 6) v = join32(v, op);
+    return v;
+}
+
 // The scale of a group whose largest |y| is amax (0 or more), and the factor that takes y to its quotient.
 //   scale = amax / qmax, at least 2^-126 (the reciprocal of a smaller one leaves fp32's range); mul = qmax / amax,
 // which is 1 / scale without scale's own rounding, so y mul is off by one rounding each of the quotient and the

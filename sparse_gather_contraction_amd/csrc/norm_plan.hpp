@@ -122,12 +122,13 @@ inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
         g.vec = flat ? 1 : vmax;
         // Channels a thread, then as many lanes along the points as the workgroup has threads for: a run of
         // 64 lanes x 16 bytes of each channel at most.
-        const int pmax = bwd || D <= 128 ? 4 : 8;
-        g.per = D >= 8 ? pmax : D >= 4 ? 2 : 1;
+        g.per = D >= 16 && !bwd ? 8 : D >= 8 ? 4 : D >= 4 ? 2 : 1;
         const int64_t ng = ceil_div64(D, g.per);
         int lg = bwd && esz == 2 && !flat ? 5 : 6;  // the backward's LDS holds two sums a point
         while (lg < 8 && (ng << lg) < 256) ++lg;
         while (lg > 2 && (ng << lg) > kNormMaxThreads) --lg;
+        // shorter runs where the points would not give every CU two tiles
+        while (!flat && lg > 4 && N * ceil_div64(M, (int64_t)g.vec << lg) < 512) --lg;
         if ((ng << lg) > kNormMaxThreads) {
             g.loop = 1;
         } else {
