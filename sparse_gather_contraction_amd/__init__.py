@@ -423,7 +423,7 @@ def disco_rms_norm_bwd(h, w, gy, gh=None, axis=1, eps=1e-6, gx=None, dw=None, wo
 
 
 def _flat_descs(tensors):
-    """An array of TensorDesc, each tensor as its elements in a row."""
+    """An array of TensorDesc as rows of 7 int64, each tensor as its elements in a row."""
     tensor = _torch.Tensor
     if not all(map(tensor.is_contiguous, tensors)):
         raise ValueError("disco tensors must be contiguous")
@@ -444,8 +444,8 @@ def _grad_workspace(grads, device):
     f, n = _entry("disco_grad_norm_workspace"), ctypes.c_size_t()
     if device is None:
         device = grads[0].device if grads else _torch.device("cuda", _torch.cuda.current_device())
-    a = _flat_descs(grads)
-    _check(f(len(grads), a.ctypes.data, n))
+    a = _flat_descs(grads).tobytes()
+    _check(f(len(grads), a, n))
     return a, _torch.empty((), dtype=_torch.float32, device=device), _torch.empty(n.value, dtype=_torch.uint8, device=device)
 
 
@@ -455,7 +455,7 @@ def disco_grad_norm(grads, device=None):
     The tensors may differ in shape and type (fp32, bf16, fp16); squares are summed in fp64."""
     f, grads = _entry("disco_grad_norm"), list(grads)
     a, norm, ws = _grad_workspace(grads, device)
-    _check(f(len(grads), a.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(), _raw_stream(norm)))
+    _check(f(len(grads), a, _desc(norm), ws.data_ptr(), ws.numel(), _raw_stream(norm)))
     return norm
 
 
@@ -470,7 +470,7 @@ def disco_clip_grads(grads, max_norm, out=None, eps=1e-6, device=None):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have one tensor for each gradient")
-        o = _flat_descs(out)
-    _check(f(len(grads), a.ctypes.data, max_norm, eps, o.ctypes.data, _desc(norm), ws.data_ptr(), ws.numel(),
+        o = _flat_descs(out).tobytes()
+    _check(f(len(grads), a, max_norm, eps, o, _desc(norm), ws.data_ptr(), ws.numel(),
              _raw_stream(norm)))
     return norm

@@ -13,48 +13,69 @@ namespace disco {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;   // vectors that a thread has in flight
 
-// The last tensor whose first chunk is not past `id` (empty tensors have no chunks and share the next one's first).
-__device__ __forceinline__ int find_tensor(const GradBatch &b, int id)
+// The tensors' first chunks, held over the lanes of each wave: two a lane.
+struct Firsts {
+    int32_t lo, hi;
+};
+
+__device__ __forceinline__ Firsts load_firsts(const GradBatch &b)
 {
-    int lo = 0, hi = b.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (b.t[mid].first <= id) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    const int l = threadIdx.x & 63;
+    Firsts f;
+    f.lo = l < b.count ? b.t[l].first : INT32_MAX;
+    f.hi = l + 64 < b.count ? b.t[l + 64].first : INT32_MAX;
+    return f;
 }
 
-template <typename T>
-__device__ __forceinline__ double sum_squares(const T *p, int n)
+// The tensor of chunk `id`: the last one whose first chunk is not past it.
+__device__ __forceinline__ int find_tensor(const Firsts &f, int id)
 {
-    constexpr int V = 16 / (int)sizeof(T), U = 4;
-    const int t = threadIdx.x;
-    double s0 = 0.0, s1 = 0.0;
-    int i = t * V;
-    for (; i + (U - 1) * kThreads * V + V <= n; i += U * kThreads * V) {
-        Pack<T, V> r[U];
+    return __popcll(__ballot(f.lo <= id)) + __popcll(__ballot(f.hi <= id)) - 1;
+}
+
+// Calls body(packs, at, full) for each run of kUnroll vectors a thread holds of p[0..n); `full`: all are whole
+// vectors inside, else vector u is one only if at + u * kThreads * V + V <= n.
+template <typename T, bool NT, typename F>
+__device__ __forceinline__ void walk(const T *p, int n, F body)
+{
+    constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
+    for (int i0 = 0; i0 + V <= n; i0 += kUnroll * S) {
+        const int i = i0 + (int)threadIdx.x * V;
+        Pack<T, V> r[kUnroll];
+        if (i0 + kUnroll * S <= n) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = load_pack<T, V>(p + i + u * kThreads * V);
+            for (int u = 0; u < kUnroll; ++u) r[u] = load_pack<T, V, NT>(p + i + u * S);
+            body(r, i, true);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float f[V];
-            unpack(r[u], f);
-#pragma unroll
-            for (int e = 0; e < V; e += 2) {
-                s0 = __builtin_fma((double)f[e], (double)f[e], s0);
-                s1 = __builtin_fma((double)f[e + 1], (double)f[e + 1], s1);
-            }
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * S + V <= n) r[u] = load_pack<T, V, NT>(p + i + u * S);
+            body(r, i, false);
         }
     }
-    for (; i + V <= n; i += kThreads * V) {
-        float f[V];
-        load_f32<T, V>(p + i, f);
+}
+
+template <typename T, bool NT>
+__device__ __forceinline__ double sum_squares(const T *p, int n)
+{
+    constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
+    double s0 = 0.0, s1 = 0.0;
+    walk<T, NT>(p, n, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) s0 = __builtin_fma((double)f[e], (double)f[e], s0);
-    }
-    const int tail = n - n % V + t;
+        for (int u = 0; u < kUnroll; ++u)
+            if (full || i + u * S + V <= n) {
+                float f[V];
+                unpack(r[u], f);
+#pragma unroll
+                for (int e = 0; e < V; e += 2) {
+                    s0 = __builtin_fma((double)f[e], (double)f[e], s0);
+                    s1 = __builtin_fma((double)f[e + 1], (double)f[e + 1], s1);
+                }
+            }
+    });
+    const int tail = n - n % V + (int)threadIdx.x;
     if (tail < n) {
         const double f = load_elem(p, tail);
         s1 = __builtin_fma(f, f, s1);
@@ -62,33 +83,22 @@ __device__ __forceinline__ double sum_squares(const T *p, int n)
     return s0 + s1;
 }
 
-template <typename T>
+template <typename T, bool NT>
 __device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k)
 {
-    constexpr int V = 16 / (int)sizeof(T), U = 4;
-    const int t = threadIdx.x;
-    int i = t * V;
-    for (; i + (U - 1) * kThreads * V + V <= n; i += U * kThreads * V) {
-        Pack<T, V> r[U];
+    constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
+    walk<T, NT>(p, n, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = load_pack<T, V>(p + i + u * kThreads * V);
+        for (int u = 0; u < kUnroll; ++u)
+            if (full || i + u * S + V <= n) {
+                float f[V];
+                unpack(r[u], f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float f[V];
-            unpack(r[u], f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) f[e] *= k;
-            store_f32<T, V>(o + i + u * kThreads * V, f);
-        }
-    }
-    for (; i + V <= n; i += kThreads * V) {
-        float f[V];
-        load_f32<T, V>(p + i, f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) f[e] *= k;
-        store_f32<T, V>(o + i, f);
-    }
-    const int tail = n - n % V + t;
+                for (int e = 0; e < V; ++e) f[e] *= k;
+                store_f32<T, V, NT>(o + i + u * S, f);
+            }
+    });
+    const int tail = n - n % V + (int)threadIdx.x;
     if (tail < n) store_elem(o, tail, load_elem(p, tail) * k);
 }
 
@@ -105,18 +115,25 @@ __device__ __forceinline__ double block_sum(double v)
     return v;
 }
 
+template <typename T>
+__device__ __forceinline__ double sum_tensor(const GradTensor &t, int64_t off, int n, bool nt)
+{
+    const T *p = (const T *)t.p + off;
+    return nt ? sum_squares<T, true>(p, n) : sum_squares<T, false>(p, n);
+}
+
 __global__ __launch_bounds__(kThreads) void grad_partial_kernel(GradBatch b, double *partial)
 {
+    const Firsts firsts = load_firsts(b);
     double s = 0.0;
     for (int id = blockIdx.x; id < b.chunks; id += gridDim.x) {
-        const int i = find_tensor(b, id);
-        const int64_t off = (int64_t)(id - b.t[i].first) * b.chunk, left = b.t[i].n - off;
+        const GradTensor &t = b.t[find_tensor(firsts, id)];
+        const int64_t off = (int64_t)(id - t.first) * b.chunk, left = t.n - off;
         const int n = (int)(left < b.chunk ? left : b.chunk);
-        const void *p = b.t[i].p;
-        switch (b.t[i].dtype) {
-        case 0: s += sum_squares((const float *)p + off, n); break;
-        case 1: s += sum_squares((const bf16_t *)p + off, n); break;
-        default: s += sum_squares((const f16_t *)p + off, n); break;
+        switch (t.dtype) {
+        case 0: s += sum_tensor<float>(t, off, n, b.stream); break;
+        case 1: s += sum_tensor<bf16_t>(t, off, n, b.stream); break;
+        default: s += sum_tensor<f16_t>(t, off, n, b.stream); break;
         }
     }
     s = block_sum(s);
@@ -139,25 +156,34 @@ __global__ __launch_bounds__(kThreads) void grad_total_kernel(double *partial, i
     }
 }
 
+template <typename T>
+__device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, int n, float k, bool nt)
+{
+    const T *p = (const T *)t.p + off;
+    T *o = (T *)t.o + off;
+    if (nt) scale_chunk<T, true>(p, o, n, k);
+    else scale_chunk<T, false>(p, o, n, k);
+}
+
 // Chunks are walked from the last to the first: the ones that the sum read last are still in the caches.
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, const double *partial, int n, float *norm,
                                                               float max_norm, float eps)
 {
+    const Firsts firsts = load_firsts(b);
     const double total = sqrt(total_of(partial, n));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
     const double c = (double)max_norm / (total + (double)eps);
     const float k = (float)(c >= 1.0 ? 1.0 : c);  // a NaN norm gives NaN
     for (int id0 = blockIdx.x; id0 < b.chunks; id0 += gridDim.x) {
-        const int id = b.chunks - 1 - id0, i = find_tensor(b, id);
-        const int64_t off = (int64_t)(id - b.t[i].first) * b.chunk, left = b.t[i].n - off;
+        const int id = b.chunks - 1 - id0;
+        const GradTensor &t = b.t[find_tensor(firsts, id)];
+        const int64_t off = (int64_t)(id - t.first) * b.chunk, left = t.n - off;
         const int len = (int)(left < b.chunk ? left : b.chunk);
-        const void *p = b.t[i].p;
-        void *o = b.t[i].o;
-        if (p == o && k == 1.0f) continue;  // in place and unchanged
-        switch (b.t[i].dtype) {
-        case 0: scale_chunk((const float *)p + off, (float *)o + off, len, k); break;
-        case 1: scale_chunk((const bf16_t *)p + off, (bf16_t *)o + off, len, k); break;
-        default: scale_chunk((const f16_t *)p + off, (f16_t *)o + off, len, k); break;
+        if (t.p == t.o && k == 1.0f) continue;  // in place and unchanged
+        switch (t.dtype) {
+        case 0: scale_tensor<float>(t, off, len, k, b.stream); break;
+        case 1: scale_tensor<bf16_t>(t, off, len, k, b.stream); break;
+        default: scale_tensor<f16_t>(t, off, len, k, b.stream); break;
         }
     }
 }

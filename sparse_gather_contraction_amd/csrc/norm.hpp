@@ -45,7 +45,7 @@ struct DequantLaunch {
 
 hipError_t launch_dequant(const DequantLaunch &a, hipStream_t stream);
 
-// One tensor of a launch over many: `n` elements at `p`, written to `o` by the scaling pass.
+// One run of a launch over many: `n` elements at `p`, written to `o` by the scaling pass.
 struct GradTensor {
     const void *p;
     void *o;
@@ -54,8 +54,8 @@ struct GradTensor {
     int32_t dtype;
 };
 
-constexpr int kGradBatch = 120;     // tensors a launch takes in its arguments (32 bytes each, below 4 KiB)
-constexpr int kGradBlocks = 1024;   // workgroups of one norm launch, so partial sums it leaves
+constexpr int kGradBatch = 120;     // runs a launch takes in its arguments (32 bytes each, below 4 KiB; 128 at most)
+constexpr int kGradBlocks = 2048;   // workgroups of one norm launch, so partial sums it leaves
 constexpr int kGradDirect = 2048;   // up to so many partial sums, each scaling workgroup adds them itself
 
 struct GradBatch {
@@ -63,6 +63,7 @@ struct GradBatch {
     int32_t count;
     int32_t chunks;
     int32_t chunk;   // elements of a chunk
+    int32_t stream;  // loads and stores that the caches drop first
 };
 
 hipError_t launch_grad_partials(const GradBatch &b, int32_t blocks, double *partial, hipStream_t stream);

@@ -19,7 +19,21 @@ struct Pack {
     uint32_t w[kWords];
 };
 
-template <typename T, int VEC>
+// A load that the caches keep, or (NT) one that is dropped by them first.
+template <bool NT, typename V, typename T>
+__device__ __forceinline__ V load_as(const T *p)
+{
+    V v;
+    if constexpr (NT) {
+        typedef V VU __attribute__((aligned(1)));
+        v = __builtin_nontemporal_load((const VU *)p);
+    } else {
+        __builtin_memcpy(&v, p, sizeof(V));
+    }
+    return v;
+}
+
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
 {
     constexpr int B = Pack<T, VEC>::kBytes;
@@ -27,16 +41,14 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
     if constexpr (B >= 16) {
 #pragma unroll
         for (int i = 0; i < B / 16; ++i) {
-            u32x4 v;
-            __builtin_memcpy(&v, p + i * (16 / (int)sizeof(T)), 16);
+            const u32x4 v = load_as<NT, u32x4>(p + i * (16 / (int)sizeof(T)));
             r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
         }
     } else if constexpr (B == 8) {
-        u32x2 v;
-        __builtin_memcpy(&v, p, 8);
+        const u32x2 v = load_as<NT, u32x2>(p);
         r.w[0] = v.x; r.w[1] = v.y;
     } else if constexpr (B == 4) {
-        __builtin_memcpy(&r.w[0], p, 4);
+        r.w[0] = load_as<NT, uint32_t>(p);
     } else if constexpr (B == 2) {
         r.w[0] = *(const uint16_t *)p;
     } else {
