@@ -1,8 +1,10 @@
 // kernels_norm_bwd.hip — backward of the root-mean-square norm.
 //
 // With h the stored sum, g = gy w, rstd = (mean_d h^2 + eps)^(-1/2):
-//   gx = rstd g - h rstd^3 mean_d(g h)  (+ gh, the gradient that reaches h past the norm)
-//   dw[d] = sum over all points of gy h rstd
+//   gx = rstd (g - u c) (+ gh, the gradient that reaches h past the norm),  u = h rstd,  c = rstd mean_d(g h)
+//   dw[d] = sum over all points of gy u
+// u is of the order of 1 and c of the order of g, so nothing on the way leaves fp32's range where h^2 does not
+// (rstd^3 does: from |h| = 2^42 on it has no normal fp32 value).
 //
 // Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
 // registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
@@ -25,8 +27,16 @@ struct BwdArgs {
     float eps;
 };
 
+// v, which the compiler takes for a new value: addresses made from it are made where they are used, and hold no
+// registers from one tile to the next.
+__device__ __forceinline__ int fresh(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Columns (M > 1): the forward's tiles.  LDS: [parts][P] sums of h^2, [parts][P] of g h, [P] rstd,
-// [P] rstd^3 mean(g h); at the end [waves of one g][channels] of dw.
+// [P] c; at the end [waves of one g][channels] of dw.
 template <typename T, int VEC, int CPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 {
@@ -42,23 +52,31 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
         w[j] = c0 + j < a.D ? load_weight<T>(a.w, a.wf32, c0 + j) : 0.0f;
         acc[j] = 0.0f;
     }
-    for (int64_t i = blockIdx.x; i < a.tiles; i += gridDim.x) {
-        const int64_t tile = NT ? i : xcd_tile(i, a.tiles);
-        const ColPos pos = col_pos(tile, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
-        const int64_t base = pos.n * a.D * a.M + pos.m;
-        Pack<T, VEC> ph[CPT], pg[CPT], pr[CPT];
+    Pack<T, VEC> ph[CPT], pg[CPT], pr[CPT];
+    ColPos pos = {0, 0, 0};
+    int64_t base = 0;
+    auto load_tile = [&](int64_t i) {
+        pos = col_pos(NT ? i : xcd_tile(i, a.tiles), lane, VEC, a.lg, a.tiles_n, a.N, a.M);
+        base = pos.n * a.D * a.M + pos.m;
+        const int c = fresh(c0);
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-            const int64_t o = base + (int64_t)(c0 + j < a.D ? c0 + j : a.D - 1) * a.M;
+            const int64_t o = base + (int64_t)(c + j < a.D ? c + j : a.D - 1) * a.M;
             ph[j] = load_pack<T, VEC>((const T *)a.h + o);
             pg[j] = load_pack<T, VEC>((const T *)a.gy + o);
         }
+    };
+    if (blockIdx.x < a.tiles) load_tile(blockIdx.x);
+    for (int64_t i = blockIdx.x; i < a.tiles; i += gridDim.x) {
         float hh[VEC], gh[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) hh[e] = gh[e] = 0.0f;
+        if (c0 + CPT > a.D)  // what was loaded in the place of channels past the end adds nothing
+#pragma unroll
+            for (int j = 0; j < CPT; ++j)
+                if (c0 + j >= a.D) ph[j] = pg[j] = {};
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-            if (c0 + j >= a.D) continue;
             float h[VEC], gy[VEC];
             unpack(ph[j], h);
             unpack(pg[j], gy);
@@ -89,15 +107,16 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
             }
             const float r = rsqrtf(u / (float)a.D + a.eps);
             rs[p] = r;
-            cs[p] = r * r * r * (v / (float)a.D);
+            cs[p] = r * (v / (float)a.D);
         }
         __syncthreads();
         // gh is asked for only now: loaded with the others it takes registers from them and bandwidth at the
         // moment when the sums wait for h and gy (888 against 802 us at 2x256x721x1440 bf16).
         if constexpr (RES) {
+            const int c = fresh(c0);
 #pragma unroll
             for (int j = 0; j < CPT; ++j)
-                pr[j] = load_pack<T, VEC>((const T *)a.gh + base + (int64_t)(c0 + j < a.D ? c0 + j : a.D - 1) * a.M);
+                pr[j] = load_pack<T, VEC>((const T *)a.gh + base + (int64_t)(c + j < a.D ? c + j : a.D - 1) * a.M);
         }
         float rstd[VEC], c[VEC];
 #pragma unroll
@@ -112,15 +131,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
         }
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-            if (c0 + j >= a.D) continue;
             float h[VEC], gy[VEC], o[VEC];
             unpack(ph[j], h);
             unpack(pg[j], gy);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float hr = h[e] * rstd[e];
-                acc[j] = e >= pos.dup ? __builtin_fmaf(gy[e], hr, acc[j]) : acc[j];
-                o[e] = rstd[e] * (gy[e] * w[j]) - h[e] * c[e];
+                const float u = h[e] * rstd[e];
+                acc[j] = e >= pos.dup ? __builtin_fmaf(gy[e], u, acc[j]) : acc[j];
+                o[e] = rstd[e] * (gy[e] * w[j] - u * c[e]);
             }
             if constexpr (RES) {
                 float r[VEC];
@@ -128,8 +146,17 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) o[e] += r[e];
             }
-            store_f32<T, VEC, NT>((T *)a.gx + base + (int64_t)(c0 + j) * a.M, o);
+            pack(o, pr[j]);
+            keep_here(pr[j]);  // one channel's fp32 values at a time
+            keep_here(acc[j]);
         }
+        // The next tile is asked for before this one's stores, in the registers that this one has left.
+        T *gx = (T *)a.gx + base;
+        if (i + gridDim.x < a.tiles) load_tile(i + gridDim.x);
+        const int c1 = fresh(c0);
+#pragma unroll
+        for (int j = 0; j < CPT; ++j)
+            if (c1 + j < a.D) store_pack<T, VEC, NT>(gx + (int64_t)(c1 + j) * a.M, pr[j]);
     }
     const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
 #pragma unroll
@@ -212,7 +239,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
                 }
         }
         s = row_sum2(s, a.lg, slots);
-        const float rstd = rsqrtf(s.u / (float)a.D + a.eps), c = rstd * rstd * rstd * (s.v / (float)a.D);
+        const float rstd = rsqrtf(s.u / (float)a.D + a.eps), c = rstd * (s.v / (float)a.D);
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             keep_packed(ph[k]);
@@ -226,9 +253,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
             unpack(pg[k], gy);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float hr = h[e] * rstd;
-                acc[k][e] = live && e >= pos[k].dup ? __builtin_fmaf(gy[e], hr, acc[k][e]) : acc[k][e];
-                o[e] = rstd * (gy[e] * w[k][e]) - h[e] * c;
+                const float u = h[e] * rstd;
+                acc[k][e] = live && e >= pos[k].dup ? __builtin_fmaf(gy[e], u, acc[k][e]) : acc[k][e];
+                o[e] = rstd * (gy[e] * w[k][e] - u * c);
             }
             if constexpr (RES) {
                 float r[VEC];
@@ -292,13 +319,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
             __syncthreads();
         }
         const float rstd = rsqrtf(s_hh[lane] / (float)a.D + a.eps);
-        const float k = rstd * rstd * rstd * (s_gh[lane] / (float)a.D);
+        const float k = rstd * (s_gh[lane] / (float)a.D);
         for (int c = g; c < a.D; c += groups) {
             const float h = load_elem(hp, (int64_t)c * a.M), gy = load_elem(gp, (int64_t)c * a.M);
-            float o = rstd * (gy * load_weight<T>(a.w, a.wf32, c)) - h * k;
+            const float u = h * rstd;
+            float o = rstd * (gy * load_weight<T>(a.w, a.wf32, c) - u * k);
             if constexpr (RES) o += load_elem((const T *)a.gh + base, (int64_t)c * a.M);
             store_elem((T *)a.gx + base, (int64_t)c * a.M, o);
-            float d = pos.dup ? 0.0f : gy * (h * rstd);
+            float d = pos.dup ? 0.0f : gy * u;
             for (int i = 1; i < P; i <<= 1) d += __shfl_xor(d, i);  // P <= 64 lanes of one wave walk together
             if (lane == 0) mine[c] = tile == blockIdx.x ? d : mine[c] + d;
         }
@@ -313,8 +341,13 @@ __global__ __launch_bounds__(1024) void dw_sum_kernel(const float *partial, int 
     const int col = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
     double s = 0.0;
     if (c < D) {
-#pragma unroll 8
-        for (int i = r0; i < blocks; i += 64) s += (double)partial[(int64_t)i * D + c];
+        for (int i = r0; i < blocks; i += 8 * 64) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = i + u * 64 < blocks ? partial[(int64_t)(i + u * 64) * D + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += (double)v[u];
+        }
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);

@@ -102,6 +102,16 @@ __device__ __forceinline__ void keep_packed(Pack<T, VEC> &r)
         for (int i = 0; i < Pack<T, VEC>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
 }
 
+// The values are made here and not put off until they are used.
+__device__ __forceinline__ void keep_here(float &v) { asm volatile("" : "+v"(v)); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ void keep_here(Pack<T, VEC> &r)
+{
+#pragma unroll
+    for (int i = 0; i < Pack<T, VEC>::kWords; ++i) asm volatile("" : "+v"(r.w[i]));
+}
+
 template <int VEC>
 __device__ __forceinline__ void unpack(const Pack<float, VEC> &r, float (&f)[VEC])
 {
