@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 
@@ -306,48 +305,24 @@ def disco_fused_conv_bwd_saved(psi: Psi, out, W, gy, gx=None, dW=None, workspace
 
 # ---- the operators around the convolution in a residual model's training step
 
-# A call on little data is bound by the host, so these wrappers pass each TensorDesc as its packed bytes.
-
-_pack = struct.Struct("Pii5q").pack  # TensorDesc
-_PAD = [(0,) * (5 - n) for n in range(6)]
-_torch = None
-_codes = {}     # torch dtype -> disco_dtype
-_fast = {}      # entry points that take packed descriptors
+BIND_PATH = os.path.join(_PKG, "_disco_bind.so")
+_bind = None
 
 
-def _entry(name):
-    """The library's function `name` with descriptors passed as bytes (or None)."""
-    global _torch
-    f = _fast.get(name)
-    if f is None:
+def _binding():
+    """The compiled marshalling of these operators (csrc/bind.cpp); raise if it has not been built."""
+    global _bind
+    if _bind is None:
         import torch
 
-        _torch = torch
-        _codes.update({torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16,
-                       torch.float8_e4m3fn: DISCO_F8_E4M3, torch.float8_e5m2: DISCO_F8_E5M2})
-        lib = load_library()
-        f = lib[name]
-        f.argtypes = [ctypes.c_void_p if t is ctypes.POINTER(TensorDesc) else t for t in getattr(lib, name).argtypes]
-        f.restype = ctypes.c_int
-        _fast[name] = f
-    return f
+        load_library()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"{BIND_PATH} is not built; run `python -m sparse_gather_contraction_amd.build`")
+        from . import _disco_bind as bind
 
-
-def _desc(t):
-    """The packed TensorDesc of a contiguous tensor of any of the library's types."""
-    if not t.is_contiguous():
-        raise ValueError("disco tensors must be contiguous")
-    shape = t.shape
-    n = len(shape)
-    if n > 5:  # refused by the library
-        shape = shape[:5]
-    return _pack(t.data_ptr(), _codes.get(t.dtype, 99), n, *shape, *_PAD[len(shape)])
-
-
-def _raw_stream(t) -> int:
-    """The current stream of the tensor's device."""
-    i = t.get_device()
-    return _torch._C._cuda_getCurrentRawStream(i) if i >= 0 else 0  # the library refuses host memory
+        bind.setup(DiscoError, torch._C._cuda_getCurrentRawStream)
+        _bind = bind
+    return _bind
 
 
 def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
@@ -355,16 +330,7 @@ def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
 
     Returns y, or (y, h) with a residual.  axis 1 normalises fields (B, C, H, W) over their channels, -1 rows
     (points, C); w (D,) is fp32 or of x's type."""
-    f = _entry("disco_rms_norm")
-    if y is None:
-        y = _torch.empty_like(x)
-    if residual is None:
-        _check(f(_desc(x), None, _desc(w), axis, eps, _desc(y), None if h is None else _desc(h), _raw_stream(x)))
-        return y
-    if h is None:
-        h = _torch.empty_like(x)
-    _check(f(_desc(x), _desc(residual), _desc(w), axis, eps, _desc(y), _desc(h), _raw_stream(x)))
-    return y, h
+    return (_bind or _binding()).rms_norm(x, w, residual, axis, eps, y, h)
 
 
 def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None, q=None, scale=None, h=None):
@@ -372,34 +338,39 @@ def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None
 
     q is of `dtype` (torch.float8_e4m3fn, the default, or torch.float8_e5m2); scale (fp32) has x's shape with the axis
     replaced by the number of runs of `group` entries (0: one run, the whole axis; else a multiple of 32)."""
-    f = _entry("disco_rms_norm_f8")
-    if q is None:
-        q = _torch.empty_like(x, dtype=dtype or _torch.float8_e4m3fn)
-    if scale is None:
-        shape = list(x.shape)
-        shape[axis] = -(-shape[axis] // group) if group > 0 else 1
-        scale = _torch.empty(shape, dtype=_torch.float32, device=x.device)
-    if residual is not None and h is None:
-        h = _torch.empty_like(x)
-    _check(f(_desc(x), None if residual is None else _desc(residual), _desc(w), axis, eps, group, _desc(q),
-             _desc(scale), None if h is None else _desc(h), _raw_stream(x)))
-    return (q, scale) if residual is None else (q, scale, h)
+    code = 0 if dtype is None or q is not None else _f8_code(dtype)
+    return (_bind or _binding()).rms_norm_f8(x, w, residual, axis, eps, group, code, q, scale, h)
+
+
+def _f8_code(dtype):
+    import torch
+
+    if dtype == torch.float8_e4m3fn:
+        return 0
+    if dtype == torch.float8_e5m2:
+        return 1
+    raise DiscoError(3, "q must be e4m3 or e5m2")
 
 
 def disco_dequantize(q, scale, dtype=None, axis=1, group=0, out=None):
     """out = q * scale in `dtype` (default bf16): the reader of disco_rms_norm_f8's form."""
-    f = _entry("disco_dequantize")
-    if out is None:
-        out = _torch.empty_like(q, dtype=dtype or _torch.bfloat16)
-    _check(f(_desc(q), _desc(scale), axis, group, _desc(out), _raw_stream(q)))
-    return out
+    code = DISCO_BF16 if dtype is None or out is not None else _data_code(dtype)
+    return (_bind or _binding()).dequantize(q, scale, code, axis, group, out)
+
+
+def _data_code(dtype):
+    import torch
+
+    code = {torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16}.get(dtype)
+    if code is None:
+        raise DiscoError(3, "out has an unsupported dtype")
+    return code
 
 
 def disco_rms_norm_bwd_workspace(h, axis=1) -> int:
     """Workspace bytes disco_rms_norm_bwd needs for this h."""
     n = ctypes.c_size_t()
-    f = _entry("disco_rms_norm_bwd_workspace")
-    _check(f(_desc(h), axis, n))
+    _check(load_library().disco_rms_norm_bwd_workspace(ctypes.byref(tensor_desc(h)), axis, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -408,69 +379,29 @@ def disco_rms_norm_bwd(h, w, gy, gh=None, axis=1, eps=1e-6, gx=None, dw=None, wo
 
     gh is the gradient that reaches h past the norm; gx is the gradient of x and of the residual alike.  The
     workspace (a uint8 device tensor) is allocated here when not given."""
-    f, g, n = _entry("disco_rms_norm_bwd"), _entry("disco_rms_norm_bwd_workspace"), ctypes.c_size_t()
-    if gx is None:
-        gx = _torch.empty_like(h)
-    if dw is None:
-        dw = _torch.empty_like(w)
-    d = _desc(h)
-    if workspace is None:
-        _check(g(d, axis, n))
-        workspace = _torch.empty(n.value or 1, dtype=_torch.uint8, device=h.device)
-    _check(f(d, _desc(w), _desc(gy), None if gh is None else _desc(gh), axis, eps, _desc(gx), _desc(dw),
-             workspace.data_ptr(), workspace.numel(), _raw_stream(h)))
-    return gx, dw
+    return (_bind or _binding()).rms_norm_bwd(h, w, gy, gh, axis, eps, gx, dw, workspace)
 
 
-def _flat_descs(tensors):
-    """An array of TensorDesc as rows of 7 int64, each tensor as its elements in a row."""
-    tensor = _torch.Tensor
-    if not all(map(tensor.is_contiguous, tensors)):
-        raise ValueError("disco tensors must be contiguous")
-    a = np.zeros((len(tensors) or 1, 7), np.int64)
-    if tensors:
-        a[:, 0] = list(map(tensor.data_ptr, tensors))
-        kinds = {t.dtype for t in tensors}
-        if len(kinds) == 1:
-            a[:, 1] = _codes.get(kinds.pop(), 99) | 1 << 32
-        else:
-            a[:, 1] = [_codes.get(t.dtype, 99) | 1 << 32 for t in tensors]
-        a[:, 2] = list(map(tensor.numel, tensors))
-    return a
+def _result_on(grads, device):
+    """A tensor for the norm where the list alone does not say its device."""
+    if device is None and len(grads):
+        return None
+    import torch
 
-
-def _grad_workspace(grads, device):
-    """(descriptors, norm, workspace) of a call on the list `grads`."""
-    f, n = _entry("disco_grad_norm_workspace"), ctypes.c_size_t()
-    if device is None:
-        device = grads[0].device if grads else _torch.device("cuda", _torch.cuda.current_device())
-    a = _flat_descs(grads).tobytes()
-    _check(f(len(grads), a, n))
-    return a, _torch.empty((), dtype=_torch.float32, device=device), _torch.empty(n.value, dtype=_torch.uint8, device=device)
+    return torch.empty((), dtype=torch.float32, device="cuda" if device is None else device)
 
 
 def disco_grad_norm(grads, device=None):
     """The norm over all elements of all tensors of the list `grads`, as a 0-dimensional fp32 tensor on their device.
 
     The tensors may differ in shape and type (fp32, bf16, fp16); squares are summed in fp64."""
-    f, grads = _entry("disco_grad_norm"), list(grads)
-    a, norm, ws = _grad_workspace(grads, device)
-    _check(f(len(grads), a, _desc(norm), ws.data_ptr(), ws.numel(), _raw_stream(norm)))
-    return norm
+    grads = grads if type(grads) is list else list(grads)
+    return (_bind or _binding()).grad_norm(grads, _result_on(grads, device))
 
 
 def disco_clip_grads(grads, max_norm, out=None, eps=1e-6, device=None):
     """Scale all gradients by min(1, max_norm / (norm + eps)), norm = disco_grad_norm(grads); returns that norm.
 
     In place, or into the tensors of the list `out`.  The factor never leaves the device."""
-    f, grads = _entry("disco_clip_grads"), list(grads)
-    a, norm, ws = _grad_workspace(grads, device)
-    o = a
-    if out is not None:
-        out = list(out)
-        if len(out) != len(grads):
-            raise ValueError("out must have one tensor for each gradient")
-        o = _flat_descs(out).tobytes()
-    _check(f(len(grads), a, max_norm, eps, o, _desc(norm), ws.data_ptr(), ws.numel(),
-             _raw_stream(norm)))
-    return norm
+    grads = grads if type(grads) is list else list(grads)
+    return (_bind or _binding()).clip_grads(grads, max_norm, eps, out, _result_on(grads, device))

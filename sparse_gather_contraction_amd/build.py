@@ -1,4 +1,4 @@
-"""Build libdisco.so (hipcc, gfx950) in-tree.
+"""Build libdisco.so (hipcc, gfx950) and the compiled part of its Python binding in-tree.
 
     python -m sparse_gather_contraction_amd.build
 """
@@ -15,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdisco.so")
+BIND = os.path.join(PKG, "_disco_bind.so")   # the marshalling of the training-step operators, on top of LIB
 PROBE_LIB = os.path.join(PKG, "libdisco_probes.so")  # microbenchmarks of the device (measurement only)
 
 SOURCES = ["plan.cpp", "plan_fused.cpp", "plan_tile.cpp", "kernels_tile.hip", "disco_api.hip", "kernels_gather.hip", "kernels_staged.hip", "kernels_fused.hip",
@@ -49,10 +50,41 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_bind() -> str:
+    """bind.cpp against Python's and torch's headers (host code, no HIP)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    obj = os.path.join(BUILD_DIR, "bind.cpp.o")
+    inc = [f"-I{d}" for d in (INCLUDE, sysconfig.get_paths()["include"], *include_paths())]
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", abi, *inc, "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj],
+                       stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for bind.cpp:\n" + r.stdout)
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + ".tmp"
+    r = subprocess.run(["g++", "-shared", obj, f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN",
+                        "-o", tmp], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link of the binding failed:\n" + r.stdout)
+    os.replace(tmp, BIND)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=4) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind_obj = bind.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -63,6 +95,7 @@ def build(verbose: bool = False) -> str:
     if missing:
         raise RuntimeError("libdisco.so has undefined symbols of its own: " + ", ".join(missing))
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     probe_obj = _compile("probes.hip")
     tmp = PROBE_LIB + ".tmp"
     r = subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", probe_obj, "-o", tmp],
@@ -71,7 +104,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("probe link failed:\n" + r.stdout)
     os.replace(tmp, PROBE_LIB)
     if verbose:
-        print("built", LIB, "and", PROBE_LIB)
+        print("built", LIB + ",", BIND, "and", PROBE_LIB)
     return LIB
 
 

@@ -160,15 +160,33 @@ def test_workspaces():
 
 
 def test_binding_refuses_strided_tensors_and_a_short_output_list():
-    a = torch.zeros((4, 6))
-    sgc._entry("disco_rms_norm")
-    with pytest.raises(ValueError):
-        sgc._desc(a.t())
-    with pytest.raises(ValueError):
-        sgc._flat_descs([a, a.t()])
-    d = sgc._flat_descs([a, torch.zeros(3, dtype=torch.bfloat16)])
-    assert d.shape == (2, 7) and d[:, 2].tolist() == [24, 3]
-    assert [int(v) & 0xffffffff for v in d[:, 1]] == [sgc.DISCO_F32, sgc.DISCO_BF16] and all(v >> 32 == 1 for v in d[:, 1])
+    a, w = torch.zeros((4, 6)), torch.ones(4)
+    for call in (lambda: sgc.disco_rms_norm(a.t(), w), lambda: sgc.disco_rms_norm(a, w, residual=a.t()),
+                 lambda: sgc.disco_rms_norm_f8(a.t(), w), lambda: sgc.disco_rms_norm_bwd(a, w, a.t()),
+                 lambda: sgc.disco_rms_norm_bwd_workspace(a.t()), lambda: sgc.disco_clip_grads([a, a.t()], 1.0),
+                 lambda: sgc.disco_grad_norm([a.t()]), lambda: sgc.disco_clip_grads([a], 1.0, out=[a.t()]),
+                 lambda: sgc.disco_clip_grads([a, a], 1.0, out=[a])):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_binding_refuses_what_is_no_tensor_and_passes_refusals_on():
+    a, w = torch.zeros((4, 6)), torch.ones(6)
+    for call in (lambda: sgc.disco_rms_norm(None, w), lambda: sgc.disco_rms_norm([1.0], w), lambda: sgc.disco_rms_norm(a, w, axis="1"),
+                 lambda: sgc.disco_clip_grads([a, 3], 1.0), lambda: sgc.disco_grad_norm(3), lambda: sgc.disco_clip_grads([a], "x")):
+        with pytest.raises(TypeError):
+            call()
+    for call, want in ((lambda: sgc.disco_rms_norm(a.long(), w), "DTYPE"), (lambda: sgc.disco_rms_norm(a, w, axis=5), "SHAPE"),
+                       (lambda: sgc.disco_rms_norm(a, w, axis=1 << 40), "SHAPE"), (lambda: sgc.disco_rms_norm(a, torch.ones(5), axis=1), "SHAPE"),
+                       (lambda: sgc.disco_rms_norm(a, w, axis=1, h=a), "INVALID_ARGUMENT"), (lambda: sgc.disco_rms_norm_f8(a, w, axis=-3), "SHAPE"),
+                       (lambda: sgc.disco_rms_norm_f8(a, w, dtype=torch.int8), "DTYPE"), (lambda: sgc.disco_rms_norm_f8(a, w, group=-32), "SHAPE"),
+                       (lambda: sgc.disco_rms_norm_f8(a, w, q=a), "DTYPE"), (lambda: sgc.disco_dequantize(a, a), "DTYPE"),
+                       (lambda: sgc.disco_dequantize(a, a, dtype=torch.int8), "DTYPE"), (lambda: sgc.disco_rms_norm_bwd(a, w, a.half()), "DTYPE"),
+                       (lambda: sgc.disco_rms_norm_bwd(a, w, a, axis=2), "SHAPE"), (lambda: sgc.disco_grad_norm([a, a.int()]), "DTYPE"),
+                       (lambda: sgc.disco_clip_grads([a], -1.0), "INVALID_ARGUMENT"), (lambda: sgc.disco_clip_grads([a], 1.0, out=[a.half()]), "DTYPE")):
+        with pytest.raises(sgc.DiscoError) as e:
+            call()
+        assert e.value.status_name == "DISCO_ERR_" + want and str(e.value), e.value
 
 
 @pytest.fixture(scope="module")
