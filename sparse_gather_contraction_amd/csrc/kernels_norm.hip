@@ -400,13 +400,13 @@ hipError_t launch_t(const NormArgs &a, const NormGeom &g, hipStream_t s)
 {
     const dim3 grid((uint32_t)g.tiles), block(g.threads);
     const size_t lds = norm_lds(g, F8 ? a.ngroups : 0);
-    // Outputs that the last-level cache cannot hold until they are read are stored past it.
     const int64_t out = a.N * a.D * a.M * ((RES ? sizeof(T) : 0) + (F8 ? 1 : sizeof(T)));
+    const int64_t run = (g.rows ? a.D : a.M) * (int64_t)(RES || !F8 ? sizeof(T) : 1);
 #define COLS(CPT) norm_cols_kernel<T, 1, CPT, RES, F8, false><<<grid, block, lds, s>>>(a)
     if (g.loop) {
         norm_loop_kernel<T, RES, F8><<<grid, block, lds, s>>>(a);
     } else if (g.vec > 1) {
-        if (out > kStreamBytes) launch_nt<T, RES, F8, true>(a, g, lds, s);
+        if (stream_stores(g.rows, out, run, a.y, a.h)) launch_nt<T, RES, F8, true>(a, g, lds, s);
         else launch_nt<T, RES, F8, false>(a, g, lds, s);
     } else if (g.rows) {
         norm_rows_kernel<T, 1, 1, RES, F8, false><<<grid, block, lds, s>>>(a);
@@ -460,8 +460,9 @@ template <typename T, int VEC, int CPT, bool NT>
 __global__ __launch_bounds__(256) void dequant_cols_kernel(DequantArgs a)
 {
     const int lane = threadIdx.x & ((1 << a.lg) - 1), g = threadIdx.x >> a.lg;
-    const int64_t tile = blockIdx.x / (uint32_t)a.chunks;
-    const int chunk = blockIdx.x % (uint32_t)a.chunks;
+    const uint32_t id = (uint32_t)xcd_tile(blockIdx.x, gridDim.x);  // 1x80x721x1440 bf16: 38.5 against 42.0 us
+    const int64_t tile = id / (uint32_t)a.chunks;
+    const int chunk = id % (uint32_t)a.chunks;
     const int c0 = (chunk * (int)(blockDim.x >> a.lg) + g) * CPT;
     if (c0 >= a.D) return;
     const ColPos pos = col_pos(tile, lane, VEC, a.lg, a.tiles_n, a.N, a.M);
@@ -513,7 +514,9 @@ hipError_t launch_dequant_t(DequantArgs a, const DequantGeom &g, hipStream_t s)
 {
     constexpr int V = 16 / (int)sizeof(T);
     const dim3 grid((uint32_t)g.blocks);
-    const bool nt = a.N * a.D * a.M * (int64_t)sizeof(T) > kStreamBytes;
+    // A wave's runs are 1 KiB here, so sectors that two tiles share are few: stores past the L2 gain with them too
+    // (1x512x361x720 72 against 90 us, rows of 512 61 against 72 us).
+    const bool nt = a.N * a.D * a.M * (int64_t)sizeof(T) > kStreamRows;
     if (a.M == 1) {
         if (!g.vec) dequant_rows_kernel<T, 1, false><<<grid, 256, 0, s>>>(a);
         else if (nt) dequant_rows_kernel<T, V, true><<<grid, 256, 0, s>>>(a);

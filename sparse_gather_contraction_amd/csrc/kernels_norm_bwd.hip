@@ -386,7 +386,7 @@ hipError_t launch_t(const BwdArgs &a, const NormGeom &g, int blocks, hipStream_t
 {
     const dim3 grid(blocks), block(g.threads);
     const size_t lds = norm_bwd_lds(g, a.D);
-    const bool nt = a.N * a.D * a.M * (int64_t)sizeof(T) > kStreamBytes;
+    const bool nt = stream_stores(g.rows, a.N * a.D * a.M * (int64_t)sizeof(T), (g.rows ? a.D : a.M) * (int64_t)sizeof(T), a.gx, nullptr);
 #define COLS(CPT) bwd_cols_kernel<T, 1, CPT, RES, false><<<grid, block, lds, s>>>(a)
     if (g.loop) {
         bwd_loop_kernel<T, RES><<<grid, block, lds, s>>>(a);

@@ -87,8 +87,19 @@ DISCO_HD RowPos row_pos(int v, int vec, int D)
 // ---- geometry
 
 constexpr int kNormMaxThreads = 1024;
-constexpr int64_t kStreamBytes = (int64_t)128 << 20;  // outputs beyond this are stored past the caches
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;  // outputs beyond these are stored past the caches: columns
+constexpr int64_t kStreamRows = (int64_t)32 << 20;    // and gradients, rows and the reader (32 MiB: all XCDs' L2)
 constexpr int kColsMinM = 64;    // fewer points after the axis than this: flat tiles of single elements
+
+// A store past the L2 leaves no line there for a neighbouring tile to complete, so what is stored must be whole
+// 64-byte sectors: `run` bytes a channel (columns) or a row, from aligned bases.  bf16, columns: the norm of
+// 2x256x721x1440 840 against 1025 us kept in the L2; with runs that end inside a sector (1x512x361x720) 356
+// against 237 us.  Between 32 and 128 MiB columns lose (2x64x360x720 39.4 against 38.5 us) and rows gain
+// (20000x4096 105 against 114 us).
+inline bool stream_stores(bool rows, int64_t bytes, int64_t run, const void *o0, const void *o1)
+{
+    return bytes > (rows ? kStreamRows : kStreamBytes) && run % 64 == 0 && (((uintptr_t)o0 | (uintptr_t)o1) & 63) == 0;
+}
 
 inline int log2_up(int64_t v)
 {
