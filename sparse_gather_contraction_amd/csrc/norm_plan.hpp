@@ -120,7 +120,7 @@ inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
         if (nv > (int64_t)kNormMaxThreads * 4) {
             g.loop = 1;
         } else {
-            g.per = nv > (bwd ? 2048 : 512) ? 4 : nv > 32 ? 2 : 1;
+            g.per = nv > (bwd ? 2048 : 512) ? 4 : nv > 8 ? 2 : 1;
             g.lg = log2_up(ceil_div64(nv, g.per));
             const int lanes = 1 << g.lg;
             g.threads = lanes > 256 ? lanes : 256;
