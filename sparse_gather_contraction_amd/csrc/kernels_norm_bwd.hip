@@ -8,8 +8,9 @@
 //
 // Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
 // registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
-// fp32 registers over the workgroup's tiles, then over its lanes, and the workgroups' partial rows are
-// summed in fp64 by a second launch; every order is fixed, so results are bitwise reproducible.
+// registers over the workgroup's tiles (a vector's terms in fp32, the vectors in fp64), then over its lanes, and
+// the workgroups' partial rows are summed in fp64 by a second launch; every order is fixed, so results are bitwise
+// reproducible.
 #include "kernels.hpp"
 #include "norm.hpp"
 #include "norm_device.hpp"
@@ -46,11 +47,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     const int lg6 = a.lg < 6 ? 6 : a.lg, parts = blockDim.x >> lg6, part = t >> lg6;
     float *s_hh = lds, *s_gh = lds + parts * P, *rs = lds + 2 * parts * P, *cs = rs + P;
     const int c0 = g * CPT;
-    float w[CPT], acc[CPT];
+    float w[CPT];
+    double acc[CPT];
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
         w[j] = c0 + j < a.D ? load_weight<T>(a.w, a.wf32, c0 + j) : 0.0f;
-        acc[j] = 0.0f;
+        acc[j] = 0.0;
     }
     Pack<T, VEC> ph[CPT], pg[CPT], pr[CPT];
     ColPos pos = {0, 0, 0};
@@ -131,15 +133,16 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
         }
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-            float h[VEC], gy[VEC], o[VEC];
+            float h[VEC], gy[VEC], o[VEC], d = 0.0f;
             unpack(ph[j], h);
             unpack(pg[j], gy);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd[e];
-                acc[j] = e >= pos.dup ? __builtin_fmaf(gy[e], u, acc[j]) : acc[j];
+                d = e >= pos.dup ? __builtin_fmaf(gy[e], u, d) : d;
                 o[e] = rstd[e] * (gy[e] * w[j] - u * c[e]);
             }
+            acc[j] += (double)d;
             if constexpr (RES) {
                 float r[VEC];
                 unpack(pr[j], r);
@@ -160,21 +163,31 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     }
     const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) acc[j] = join_run(acc[j], in_wave, AddOp());
+    for (int j = 0; j < CPT; ++j)
+        for (int o = 0; o < in_wave; ++o) acc[j] += __shfl_xor(acc[j], 1 << o);
     __syncthreads();
     if ((lane & ((1 << in_wave) - 1)) == 0)
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) lds[(lane >> 6) * width + c0 + j] = acc[j];
+        for (int j = 0; j < CPT; ++j) lds[(lane >> 6) * width + c0 + j] = (float)acc[j];
     __syncthreads();
     for (int c = t; c < a.D; c += blockDim.x) {
-        float s = lds[c];
-        for (int i = 1; i < waves; ++i) s += lds[i * width + c];
-        a.partial[(int64_t)blockIdx.x * a.D + c] = s;
+        double s = lds[c];
+        for (int i = 1; i < waves; ++i) s += (double)lds[i * width + c];
+        a.partial[(int64_t)blockIdx.x * a.D + c] = (float)s;
     }
 }
 
 struct Sum2 {
     float u, v;
+};
+
+template <bool C, typename A, typename B>
+struct If {
+    typedef A type;
+};
+template <typename A, typename B>
+struct If<false, A, B> {
+    typedef B type;
 };
 
 // Two sums over the 2^lg threads of a row.
@@ -205,14 +218,17 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
     const int t = threadIdx.x, lanes = 1 << a.lg, tt = t & (lanes - 1), slot = t >> a.lg;
     const int rows = blockDim.x >> a.lg;
     RowPos pos[KPT];
-    float w[KPT][VEC], acc[KPT][VEC];
+    // dw of a thread's elements over its rows, in fp64 where registers are left (up to two vectors a thread)
+    using Acc = typename If<KPT <= 2, double, float>::type;
+    float w[KPT][VEC];
+    Acc acc[KPT][VEC];
 #pragma unroll
     for (int k = 0; k < KPT; ++k) {
         pos[k] = row_pos(k * lanes + tt, VEC, a.D);
         if (a.wf32) load_f32<float, VEC>((const float *)a.w + pos[k].c, w[k]);
         else load_f32<T, VEC>((const T *)a.w + pos[k].c, w[k]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[k][e] = 0.0f;
+        for (int e = 0; e < VEC; ++e) acc[k][e] = 0;
     }
     Pack<T, VEC> ph[KPT], pg[KPT], pr[KPT];
     bool live = false;
@@ -261,7 +277,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd;
-                acc[k][e] = live && e >= pos[k].dup ? __builtin_fmaf(gy[e], u, acc[k][e]) : acc[k][e];
+                acc[k][e] += live && e >= pos[k].dup ? (Acc)(gy[e] * u) : (Acc)0;
                 o[e] = rstd * (gy[e] * w[k][e] - u * c);
             }
             if constexpr (RES) {
@@ -287,19 +303,19 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         for (int k = 0; k < KPT; ++k)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= pos[k].dup) lds[slot * a.D + pos[k].c + e] = acc[k][e];
+                if (e >= pos[k].dup) lds[slot * a.D + pos[k].c + e] = (float)acc[k][e];
         __syncthreads();
         for (int c = t; c < a.D; c += blockDim.x) {
-            float s = 0.0f;
-            for (int i = 0; i < rows; ++i) s += lds[i * a.D + c];
-            mine[c] = s;
+            double s = 0.0;
+            for (int i = 0; i < rows; ++i) s += (double)lds[i * a.D + c];
+            mine[c] = (float)s;
         }
     } else {
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= pos[k].dup) mine[pos[k].c + e] = acc[k][e];
+                if (e >= pos[k].dup) mine[pos[k].c + e] = (float)acc[k][e];
     }
 }
 

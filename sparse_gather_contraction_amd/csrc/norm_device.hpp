@@ -104,6 +104,7 @@ __device__ __forceinline__ void keep_packed(Pack<T, VEC> &r)
 
 // The values are made here and not put off until they are used.
 __device__ __forceinline__ void keep_here(float &v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void keep_here(double &v) { asm volatile("" : "+v"(v)); }
 
 template <typename T, int VEC>
 __device__ __forceinline__ void keep_here(Pack<T, VEC> &r)

@@ -139,6 +139,72 @@ def test_norm_bwd(case, dtype):
         close(dw, rdw, rdw.abs() * half(wdt) * 1.001 + 244 * U * sdw + floor_of(wdt), "dw")
 
 
+def bwd_reference(h, w, gy, gh, axis):
+    """gx, the bound of its fp32 steps, dw and the sum of its terms' sizes, by the formula in fp64."""
+    H, G = h.double(), gy.double() * per(w.double(), h, axis)
+    rstd = (H.square().mean(axis, keepdim=True) + EPS).rsqrt()
+    mean, size = (G * H).mean(axis, keepdim=True), (G * H).abs().mean(axis, keepdim=True)
+    a, b, c = rstd * G, H * rstd ** 3 * mean, gh.double() if gh is not None else torch.zeros_like(H)
+    bound = U * (46 * a.abs() + 134 * b.abs() + 84 * H.abs() * rstd ** 3 * size + 3 * (a.abs() + b.abs() + c.abs()))
+    terms = gy.double() * H * rstd
+    dims = [i for i in range(h.dim()) if i != axis % h.dim()]
+    return a - b + c, bound, terms.sum(dims), terms.abs().sum(dims)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 50, 2.0 ** -50])
+@pytest.mark.parametrize("case", [((40, 256), -1), ((2, 32, 16, 16), 1), ((9, 24, 3), 1), ((3, 20000), -1)], ids=ids)
+def test_norm_bwd_of_large_and_small_values(case, scale):
+    # rstd^3 leaves fp32's range at 2^50 where h^2 does not; at 2^-50 eps alone is left of the mean
+    shape, axis = case
+    print(f"[bwd] {shape} axis {axis} scale {scale}", flush=True)
+    for dt in (torch.float32, torch.bfloat16):
+        h, gy, gh = randn(shape, dt, 111, 2.0) * scale, randn(shape, dt, 112), randn(shape, dt, 113) / scale
+        w = randn((shape[axis],), torch.float32, 114)
+        gx, dw = sgc.disco_rms_norm_bwd(h, w, gy, gh=gh, axis=axis, eps=EPS)
+        ref, bound, rdw, sdw = bwd_reference(h, w, gy, gh, axis)
+        close(gx, ref, ref.abs() * half(dt) * 1.001 + bound + 1e-40, "gx")
+        close(dw, rdw, rdw.abs() * U * 1.001 + 244 * U * sdw + 1e-40, "dw")
+
+
+# Outputs beyond the sizes from which stores go past the L2: whole sectors, runs that end inside a sector, an
+# unaligned base, rows.
+LARGE = [((1, 256, 512, 520), 1, 0), ((1, 72, 721, 1441), 1, 0), ((1, 256, 512, 520), 1, 3), ((40000, 512), -1, 0), ((40000, 511), -1, 0), ((70001, 264), -1, 1)]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda v: ids(v) + f"+{v[2]}")
+def test_large_outputs(case):
+    shape, axis, shift = case
+    print(f"[large] {shape} axis {axis} shift {shift}", flush=True)
+    dt = torch.bfloat16
+    gen = torch.Generator(device=DEV).manual_seed(121)
+    n = math.prod(shape)
+    x, r, gy = (torch.randn(n + shift, generator=gen, dtype=dt, device=DEV)[shift:].view(shape) for _ in range(3))
+    w = randn((shape[axis],), torch.float32, 122)
+    y, h = (torch.empty(n + shift, dtype=dt, device=DEV)[shift:].view(shape) for _ in range(2))
+    sgc.disco_rms_norm(x, w, residual=r, axis=axis, eps=EPS, y=y, h=h)
+    q, scale, h8 = sgc.disco_rms_norm_f8(x, w, residual=r, axis=axis, eps=EPS)
+    back = sgc.disco_dequantize(q, scale, axis=axis)
+    gx, dw = sgc.disco_rms_norm_bwd(h, w, gy, gh=r, axis=axis, eps=EPS, gx=torch.empty_like(h) if shift == 0 else y.clone())
+    assert torch.equal(h8, h)
+    total = torch.zeros(shape[axis], dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(total)
+    cut = 0 if axis == -1 else 2  # in pieces: the fp64 intermediates are large
+    for lo in range(0, shape[cut], -(-shape[cut] // 8)):
+        k = min(-(-shape[cut] // 8), shape[cut] - lo)
+        X, R, GY, Y, H, B, GX = (t.narrow(cut, lo, k) for t in (x, r, gy, y, h, back, gx))
+        S = X.double() + R.double()
+        close(H, S, S.abs() * (half(dt) + U) * 1.001 + 1e-40, "h")
+        ref = S * (S.square().mean(axis, keepdim=True) + EPS).rsqrt() * per(w.double(), S, axis)
+        close(Y, ref, ref.abs() * (half(dt) + 46 * U) * 1.001 + 1e-40, "y")
+        top = ref.abs().amax(axis, keepdim=True)
+        close(B, ref, ref.abs() * (2 ** -4 + 2 ** -8) * 1.01 + top / 448 * 2.0 ** -10 * 1.01, "back")
+        gref, bound, rdw, sdw = bwd_reference(H, w, GY, R, axis)
+        close(GX, gref, gref.abs() * half(dt) * 1.001 + bound + 1e-40, "gx")
+        total += rdw
+        size += sdw
+    close(dw, total, total.abs() * U * 1.001 + 244 * U * size + 1e-40, "dw")
+
+
 def test_norm_bwd_against_differences():
     # the directional derivative of <gy, y> + <gh, h> in x and in w, by central differences in fp64 of the formula
     shape = (2, 24, 9, 15)
@@ -267,6 +333,33 @@ def test_grad_norm_and_clip(sizes, dtype):
         mine = [g.clone() for g in grads]
         sgc.disco_clip_grads(mine, max_norm)
         assert all(torch.equal(a, b) for a, b in zip(mine, outs))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gap", [0, 5])
+def test_gradients_in_one_buffer(dtype, gap):
+    # tensors that follow each other are walked as one run; the result may not depend on the outputs' places
+    sizes = [3, 257, 0, 70001, 8192, 5, 44_000_000 if gap == 0 else 100_001, 9001]
+    print(f"[clip] one buffer {dtype} gap {gap}", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(131)
+    flat = torch.randn(sum(sizes) + gap * len(sizes), generator=gen, device=DEV).to(T[dtype])
+    at = [sum(sizes[:i]) + gap * i for i in range(len(sizes))]
+    grads = [flat[a:a + n] for a, n in zip(at, sizes)]
+    ref = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    norm = sgc.disco_grad_norm(grads)
+    assert abs(float(norm) - ref) <= 2 * U * ref
+    factor = min(1.0, 0.25 / (ref + EPS))
+    into = torch.full_like(flat, 7.0)
+    apart = [torch.empty_like(g) for g in grads]
+    n1 = sgc.disco_clip_grads(grads, 0.25, out=[into[a:a + n] for a, n in zip(at, sizes)])
+    n2 = sgc.disco_clip_grads(grads, 0.25, out=apart)
+    assert float(n1) == float(norm) == float(n2)
+    for g, a, n, o in zip(grads, at, sizes, apart):
+        r = g.double() * factor
+        close(o, r, r.abs() * (half(g.dtype) + 4 * U) * 1.001 + floor_of(g.dtype), "out")
+        assert torch.equal(into[a:a + n], o) and bool((into[a + n:a + n + gap] == 7).all())
+    n3 = sgc.disco_clip_grads(grads, 0.25)
+    assert float(n3) == float(norm) and all(torch.equal(g, o) for g, o in zip(grads, apart))
 
 
 def test_grad_norm_of_none_and_of_extremes():
