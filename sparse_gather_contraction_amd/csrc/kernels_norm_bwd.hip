@@ -163,8 +163,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     }
     const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
 #pragma unroll
-    for (int j = 0; j < CPT; ++j)
-        for (int o = 0; o < in_wave; ++o) acc[j] += __shfl_xor(acc[j], 1 << o);
+    for (int j = 0; j < CPT; ++j) acc[j] = join_run(acc[j], in_wave, AddOp());
     __syncthreads();
     if ((lane & ((1 << in_wave) - 1)) == 0)
 #pragma unroll

@@ -250,7 +250,8 @@ __device__ __forceinline__ float max_abs(float m, float a, float b)
 // ---- joins over the lanes of a wave: DPP moves and the row and half swaps, which need no LDS
 
 struct AddOp {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+    template <typename V>
+    __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
 };
 struct MaxOp {  // of values that are 0 or more; a NaN is kept
     __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
@@ -262,12 +263,31 @@ __device__ __forceinline__ float dpp(float v)
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v)
+{
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const u32x2 r = {(uint32_t)__builtin_amdgcn_mov_dpp((int)w.x, CTRL, 0xf, 0xf, true),
+                     (uint32_t)__builtin_amdgcn_mov_dpp((int)w.y, CTRL, 0xf, 0xf, true)};
+    return __builtin_bit_cast(double, r);
+}
+
 // v of the lane's row of 16 and of the row beside it (lane ^ 16), in an order that both rows share
 template <typename Op>
 __device__ __forceinline__ float join16(float v, Op op)
 {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+template <typename Op>
+__device__ __forceinline__ double join16(double v, Op op)
+{
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const auto x = __builtin_amdgcn_permlane16_swap(w.x, w.x, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(w.y, w.y, false, false);
+    const u32x2 a = {x[0], y[0]}, b = {x[1], y[1]};
+    return op(__builtin_bit_cast(double, a), __builtin_bit_cast(double, b));
 }
 
 // the same over the wave's halves (lane ^ 32)
@@ -278,9 +298,19 @@ __device__ __forceinline__ float join32(float v, Op op)
     return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Joins v over each run of 2^lg lanes (lg <= 6, uniform), every lane of a run getting the same value.
 template <typename Op>
-__device__ __forceinline__ float join_run(float v, int lg, Op op)
+__device__ __forceinline__ double join32(double v, Op op)
+{
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const auto x = __builtin_amdgcn_permlane32_swap(w.x, w.x, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(w.y, w.y, false, false);
+    const u32x2 a = {x[0], y[0]}, b = {x[1], y[1]};
+    return op(__builtin_bit_cast(double, a), __builtin_bit_cast(double, b));
+}
+
+// Joins v over each run of 2^lg lanes (lg <= 6, uniform), every lane of a run getting the same value.
+template <typename V, typename Op>
+__device__ __forceinline__ V join_run(V v, int lg, Op op)
 {
     if (lg > 0) v = op(v, dpp<0xB1>(v));   // quad_perm 1 0 3 2
     if (lg > 1) v = op(v, dpp<0x4E>(v));   // quad_perm 2 3 0 1
