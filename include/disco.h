@@ -213,7 +213,8 @@ disco_status disco_fused_conv_bwd_noalloc(disco_psi h, const disco_tensor *x, co
  * into a flat buffer serve.  Outputs must overlap neither inputs nor each other
  * (DISCO_ERR_INVALID_ARGUMENT).  All statistics are fp32 or wider, each output is rounded once (RNE), and
  * results are bitwise reproducible run to run.  Nothing is allocated on the device, so every call can be
- * captured into a graph.  A tensor with no elements is accepted and nothing is launched for it. */
+ * captured into a graph.  A tensor with no elements is accepted and nothing is launched for it.
+ * Squares are fp32 sums: a row whose sum of squares passes fp32's range (|h| near 2^64 / sqrt(D)) has rstd 0. */
 
 /* Root-mean-square norm over `axis`, of x or, with `residual`, of h = x + residual:
  *   y = h * rstd * w,   rstd = (mean(h^2) + eps)^(-1/2)
@@ -255,7 +256,8 @@ disco_status disco_rms_norm_bwd(const disco_tensor *h, const disco_tensor *w, co
 /* norm = sqrt(sum of the squares of all elements of the n tensors), squares summed in fp64.  The tensors may
  * differ in shape and dtype (F32, BF16, F16) and may be empty; n may be 0 (norm 0).  norm: one F32 element.
  * `workspace`: caller-owned device memory (8-byte aligned) of at least the size disco_grad_norm_workspace
- * reports for these tensors (their data is not read), as disco_rms_norm_bwd's. */
+ * reports for these tensors (their data is not read), as disco_rms_norm_bwd's.  Tensors that follow each other in
+ * memory are walked as one; all of them together have at most 2^40 elements. */
 disco_status disco_grad_norm_workspace(int64_t n, const disco_tensor *grads, size_t *bytes);
 disco_status disco_grad_norm(int64_t n, const disco_tensor *grads, disco_tensor *norm, void *workspace,
                              size_t workspace_bytes, void *stream);

@@ -10,7 +10,10 @@ The names mirror the C ABI in ``include/disco.h``:
     gx  = disco_bwd(psi, gout)               # (B,C,K,Ho,Wo) -> (B,C,Hi,Wi)
     y   = disco_fused_conv(psi, x, W)        # (B,C,Hi,Wi), (Co,C,K) -> (B,Co,Ho,Wo)
 
-There is no fallback: if the library is not built, loading raises.
+The operators around the convolution in a training step (disco_rms_norm and below) are marshalled by a
+compiled module, ``_disco_bind.so`` (csrc/bind.cpp), in the same way.
+
+There is no fallback: if a library is not built, loading raises.
 """
 from __future__ import annotations
 
