@@ -35,14 +35,14 @@ __device__ __forceinline__ int find_tensor(const Firsts &f, int id)
     return __popcll(__ballot(f.lo <= id)) + __popcll(__ballot(f.hi <= id)) - 1;
 }
 
-// Calls body(packs, at, full) for each run of kUnroll vectors a thread holds of p[0..n); `full`: all are whole
-// vectors inside, else vector u is one only if at + u * kThreads * V + V <= n.
+// Calls body(packs, at, full) for each run of kUnroll vectors that thread t of kThreads holds of p[0..n); `full`: all
+// are whole vectors inside, else vector u is one only if at + u * kThreads * V + V <= n.
 template <typename T, bool NT, typename F>
-__device__ __forceinline__ void walk(const T *p, int n, F body)
+__device__ __forceinline__ void walk(const T *p, int n, int t, F body)
 {
     constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
     for (int i0 = 0; i0 + V <= n; i0 += kUnroll * S) {
-        const int i = i0 + (int)threadIdx.x * V;
+        const int i = i0 + t * V;
         Pack<T, V> r[kUnroll];
         if (i0 + kUnroll * S <= n) {
 #pragma unroll
@@ -58,11 +58,11 @@ __device__ __forceinline__ void walk(const T *p, int n, F body)
 }
 
 template <typename T, bool NT>
-__device__ __forceinline__ double sum_squares(const T *p, int n)
+__device__ __forceinline__ double sum_squares(const T *p, int n, int t)
 {
     constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
     double s0 = 0.0, s1 = 0.0;
-    walk<T, NT>(p, n, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
+    walk<T, NT>(p, n, t, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             if (full || i + u * S + V <= n) {
@@ -75,7 +75,7 @@ __device__ __forceinline__ double sum_squares(const T *p, int n)
                 }
             }
     });
-    const int tail = n - n % V + (int)threadIdx.x;
+    const int tail = n - n % V + t;
     if (tail < n) {
         const double f = load_elem(p, tail);
         s1 = __builtin_fma(f, f, s1);
@@ -84,10 +84,10 @@ __device__ __forceinline__ double sum_squares(const T *p, int n)
 }
 
 template <typename T, bool NT>
-__device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k)
+__device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k, int t)
 {
     constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
-    walk<T, NT>(p, n, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
+    walk<T, NT>(p, n, t, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             if (full || i + u * S + V <= n) {
@@ -98,20 +98,21 @@ __device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k)
                 store_f32<T, V, NT>(o + i + u * S, f);
             }
     });
-    const int tail = n - n % V + (int)threadIdx.x;
+    const int tail = n - n % V + t;
     if (tail < n) store_elem(o, tail, load_elem(p, tail) * k);
 }
 
-// The sum of a value over the workgroup, the same in every thread.
+// The sum of a value over the workgroup of THREADS, the same in every thread.
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double v)
 {
-    __shared__ double part[kThreads / 64];
+    __shared__ double part[THREADS / 64];
     for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) v += part[i];
+    for (int i = 0; i < THREADS / 64; ++i) v += part[i];
     return v;
 }
 
@@ -119,7 +120,7 @@ template <typename T>
 __device__ __forceinline__ double sum_tensor(const GradTensor &t, int64_t off, int n, bool nt)
 {
     const T *p = (const T *)t.p + off;
-    return nt ? sum_squares<T, true>(p, n) : sum_squares<T, false>(p, n);
+    return nt ? sum_squares<T, true>(p, n, threadIdx.x) : sum_squares<T, false>(p, n, threadIdx.x);
 }
 
 __global__ __launch_bounds__(kThreads) void grad_partial_kernel(GradBatch b, double *partial)
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void grad_partial_kernel(GradBatch b, dou
         default: s += sum_tensor<f16_t>(t, off, n, b.stream); break;
         }
     }
-    s = block_sum(s);
+    s = block_sum<kThreads>(s);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -144,7 +145,7 @@ __device__ __forceinline__ double total_of(const double *partial, int n)
 {
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-    return block_sum(s);
+    return block_sum<kThreads>(s);
 }
 
 __global__ __launch_bounds__(kThreads) void grad_total_kernel(double *partial, int n, float *norm)
@@ -161,8 +162,47 @@ __device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, i
 {
     const T *p = (const T *)t.p + off;
     T *o = (T *)t.o + off;
-    if (nt) scale_chunk<T, true>(p, o, n, k);
-    else scale_chunk<T, false>(p, o, n, k);
+    if (nt) scale_chunk<T, true>(p, o, n, k, threadIdx.x);
+    else scale_chunk<T, false>(p, o, n, k, threadIdx.x);
+}
+
+// The factor of a total norm; a NaN norm gives NaN.
+__device__ __forceinline__ float clip_factor(double total, float max_norm, float eps)
+{
+    const double c = (double)max_norm / (total + (double)eps);
+    return (float)(c >= 1.0 ? 1.0 : c);
+}
+
+// Few elements: one workgroup sums all chunks and scales them, kThreads threads a chunk.
+__global__ __launch_bounds__(1024) void grad_small_kernel(GradSmall g, GradSmall out, double *partial, float *norm,
+                                                          float max_norm, float eps)
+{
+    const int first = threadIdx.x / kThreads, t = threadIdx.x % kThreads, step = 1024 / kThreads;
+    double s = 0.0;
+    for (int i = first; i < g.count; i += step) {
+        const GradTensor &v = g.t[i];
+        switch (v.dtype) {
+        case 0: s += sum_squares<float, false>((const float *)v.p, (int)v.n, t); break;
+        case 1: s += sum_squares<bf16_t, false>((const bf16_t *)v.p, (int)v.n, t); break;
+        default: s += sum_squares<f16_t, false>((const f16_t *)v.p, (int)v.n, t); break;
+        }
+    }
+    s = block_sum<1024>(s);
+    const double total = sqrt(s);
+    if (threadIdx.x == 0) {
+        partial[0] = s;
+        *norm = (float)total;
+    }
+    const float k = clip_factor(total, max_norm, eps);
+    for (int i = first; i < out.count; i += step) {
+        const GradTensor &v = out.t[i];
+        if (v.p == v.o && k == 1.0f) continue;  // in place and unchanged
+        switch (v.dtype) {
+        case 0: scale_chunk<float, false>((const float *)v.p, (float *)v.o, (int)v.n, k, t); break;
+        case 1: scale_chunk<bf16_t, false>((const bf16_t *)v.p, (bf16_t *)v.o, (int)v.n, k, t); break;
+        default: scale_chunk<f16_t, false>((const f16_t *)v.p, (f16_t *)v.o, (int)v.n, k, t); break;
+        }
+    }
 }
 
 // Chunks are walked from the last to the first: the ones that the sum read last are still in the caches.
@@ -172,8 +212,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, const
     const Firsts firsts = load_firsts(b);
     const double total = sqrt(total_of(partial, n));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
-    const double c = (double)max_norm / (total + (double)eps);
-    const float k = (float)(c >= 1.0 ? 1.0 : c);  // a NaN norm gives NaN
+    const float k = clip_factor(total, max_norm, eps);
     for (int id0 = blockIdx.x; id0 < b.chunks; id0 += gridDim.x) {
         const int id = b.chunks - 1 - id0;
         const GradTensor &t = b.t[find_tensor(firsts, id)];
@@ -193,6 +232,13 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, const
 hipError_t launch_grad_partials(const GradBatch &b, int32_t blocks, double *partial, hipStream_t s)
 {
     grad_partial_kernel<<<dim3(blocks), kThreads, 0, s>>>(b, partial);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_small(const GradSmall &g, const GradSmall &out, double *partial, float *norm, float max_norm,
+                             float eps, hipStream_t s)
+{
+    grad_small_kernel<<<1, 1024, 0, s>>>(g, out, partial, norm, max_norm, eps);
     return hipGetLastError();
 }
 

@@ -23,6 +23,7 @@ struct BwdArgs {
     const void *h, *gy, *gh, *w;
     void *gx;
     float *partial;
+    void *dw;      // not null: the launch is one workgroup, whose sums are dw itself
     int64_t N, M, tiles;
     int32_t D, wf32, lg, tiles_n;
     float eps;
@@ -34,6 +35,15 @@ __device__ __forceinline__ int fresh(int v)
 {
     asm volatile("" : "+v"(v));
     return v;
+}
+
+// A workgroup's sum for channel c: its entry of the partial sums, or dw.
+template <typename T>
+__device__ __forceinline__ void store_dw(const BwdArgs &a, int c, double s)
+{
+    if (!a.dw) a.partial[(int64_t)blockIdx.x * a.D + c] = (float)s;
+    else if (a.wf32) ((float *)a.dw)[c] = (float)s;
+    else store_elem((T *)a.dw, c, (float)s);
 }
 
 // Columns (M > 1): the forward's tiles.  LDS: [parts][P] sums of h^2, [parts][P] of g h, [P] rstd,
@@ -172,7 +182,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     for (int c = t; c < a.D; c += blockDim.x) {
         double s = lds[c];
         for (int i = 1; i < waves; ++i) s += (double)lds[i * width + c];
-        a.partial[(int64_t)blockIdx.x * a.D + c] = (float)s;
+        store_dw<T>(a, c, s);
     }
 }
 
@@ -296,7 +306,6 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         for (int k = 0; k < KPT; ++k)
             if (pos[k].dup < VEC) store_pack<T, VEC, NT>(gx + pos[k].c, pr[k]);
     }
-    float *mine = a.partial + (int64_t)blockIdx.x * a.D;
     if (rows > 1) {
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
@@ -307,14 +316,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         for (int c = t; c < a.D; c += blockDim.x) {
             double s = 0.0;
             for (int i = 0; i < rows; ++i) s += (double)lds[i * a.D + c];
-            mine[c] = (float)s;
+            store_dw<T>(a, c, s);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= pos[k].dup) mine[pos[k].c + e] = (float)acc[k][e];
+                if (e >= pos[k].dup) store_dw<T>(a, pos[k].c + e, (double)acc[k][e]);
     }
 }
 
@@ -442,12 +451,16 @@ hipError_t launch_r(const BwdArgs &a, const NormGeom &g, bool res, int blocks, h
 
 }  // namespace
 
+// Up to two tiles are done by one workgroup, which then needs no second launch (4x617 bf16 6.4 against 10.0 us).
+static bool one_block(const NormGeom &g) { return !g.loop && g.tiles <= 2; }
+
 // 256 CUs; 1024 threads of these kernels' registers a CU, and half of them for rows: fewer rows open at a time
 // (259200x512 bf16 194 against 214 us, fp32 389 against 433 us).
 int32_t norm_bwd_blocks(int64_t N, int64_t D, int64_t M, int esz)
 {
     if (N == 0 || M == 0) return 0;
     const NormGeom g = norm_geom(N, D, M, esz, true);
+    if (one_block(g)) return 1;
     const int each = g.rows ? 512 : 1024;
     const int64_t most = 256 * (g.threads >= each ? 1 : each / g.threads);
     return (int32_t)(g.tiles < most ? g.tiles : most);
@@ -458,7 +471,9 @@ hipError_t launch_norm_bwd(const NormLaunch &l, hipStream_t s)
     const int esz = l.dtype == 0 ? 4 : 2;
     if (l.blocks > 0) {
         const NormGeom g = norm_geom(l.N, l.D, l.M, esz, true);
+        const bool one = one_block(g);
         BwdArgs a;
+        a.dw = one ? l.dw : nullptr;
         a.h = l.x; a.gy = l.gy; a.gh = l.r; a.w = l.w; a.gx = l.y; a.partial = l.partial;
         a.N = l.N; a.M = l.M; a.tiles = g.tiles;
         a.D = (int32_t)l.D; a.wf32 = l.wf32; a.lg = g.lg; a.tiles_n = g.tiles_n; a.eps = l.eps;
@@ -466,7 +481,7 @@ hipError_t launch_norm_bwd(const NormLaunch &l, hipStream_t s)
         const hipError_t e = l.dtype == 0 ? launch_r<float>(a, g, res, l.blocks, s)
                            : l.dtype == 1 ? launch_r<bf16_t>(a, g, res, l.blocks, s)
                                           : launch_r<f16_t>(a, g, res, l.blocks, s);
-        if (e != hipSuccess) return e;
+        if (e != hipSuccess || one) return e;
     }
     const dim3 grid((uint32_t)ceil_div64(l.D, 16));
     if (l.wf32) dw_sum_kernel<float><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (float *)l.dw);

@@ -296,6 +296,20 @@ void plan_grads(const std::vector<Run> &runs, int64_t total, GradPlan *p)
     for (const disco::GradBatch &b : p->batches) p->slots += blocks_of(b);
 }
 
+// The runs in chunks for one workgroup, if they are few; false otherwise.
+bool small_of(const std::vector<Run> &runs, int64_t total, disco::GradSmall *s)
+{
+    s->count = 0;
+    if (total > disco::kSmallElements) return false;
+    for (const Run &r : runs)
+        for (int64_t off = 0; off < r.n; off += disco::kSmallChunk) {
+            if (s->count == disco::kSmallChunks) return false;
+            const int64_t esz = elem_size(r.dtype);
+            s->t[s->count++] = {r.p + off * esz, r.o ? r.o + off * esz : nullptr, std::min(r.n - off, disco::kSmallChunk), 0, r.dtype};
+        }
+    return true;
+}
+
 // Partial sums that tensors of these sizes leave at most, however they lie in memory: runs of several tensors
 // have no more chunks and launches than the tensors have.
 int64_t slots_of(int64_t n, const disco_tensor *g)
@@ -397,25 +411,39 @@ disco_status grads_impl(int64_t n, const disco_tensor *grads, bool clip, float m
     // The sum's runs go by the gradients alone, so its order and result are one and the same whatever the outputs.
     std::vector<Run> runs;
     runs_of(n, grads, nullptr, &runs);
-    GradPlan p;
-    plan_grads(runs, total, &p);
     double *partial = (double *)workspace;
     hipStream_t sm = (hipStream_t)stream;
     hipError_t e = hipSuccess;
-    int64_t at = 0;
-    for (const disco::GradBatch &b : p.batches) {
-        if (e == hipSuccess) e = disco::launch_grad_partials(b, blocks_of(b), partial + at, sm);
-        at += blocks_of(b);
-    }
-    int32_t slots = (int32_t)p.slots;
     float *nd = (float *)norm->data;
-    if (e == hipSuccess && (!clip || p.batches.empty() || slots > disco::kGradDirect)) {
-        e = disco::launch_grad_total(partial, slots, nd, sm);
-        slots = slots > 0 ? 1 : 0;
+    int32_t slots = 1;  // partial sums that the scaling pass finds
+    disco::GradSmall few, scaled;
+    bool done = false;
+    if (small_of(runs, total, &few)) {
+        scaled.count = 0;
+        if (clip) {
+            runs_of(n, grads, outs, &runs);
+            done = small_of(runs, total, &scaled);
+            if (!done) scaled.count = 0;
+        }
+        e = disco::launch_grad_small(few, scaled, partial, nd, max_norm, eps, sm);
         nd = nullptr;
+    } else {
+        GradPlan p;
+        plan_grads(runs, total, &p);
+        int64_t at = 0;
+        for (const disco::GradBatch &b : p.batches) {
+            if (e == hipSuccess) e = disco::launch_grad_partials(b, blocks_of(b), partial + at, sm);
+            at += blocks_of(b);
+        }
+        slots = (int32_t)p.slots;
+        if (e == hipSuccess && (!clip || slots > disco::kGradDirect)) {
+            e = disco::launch_grad_total(partial, slots, nd, sm);
+            slots = 1;
+            nd = nullptr;
+        }
+        if (clip) runs_of(n, grads, outs, &runs);
     }
-    if (clip) {
-        runs_of(n, grads, outs, &runs);
+    if (clip && !done) {
         GradPlan q;
         plan_grads(runs, total, &q);
         for (size_t i = 0; i < q.batches.size() && e == hipSuccess; ++i) {
