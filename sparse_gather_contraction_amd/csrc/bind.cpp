@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <vector>
@@ -139,8 +140,8 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f)
     try {
         return f();
     } catch (const Raised &) {
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own, as the exceptions that its users know (out of memory among them)
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

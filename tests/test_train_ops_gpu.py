@@ -422,6 +422,45 @@ def test_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(held, eager)), f"replay {k}"
 
 
+def test_graph_replays_of_small_calls():
+    # the forms of one launch: a backward of one tile, gradients that one workgroup sums and scales
+    x, gy = randn((4, 617), torch.bfloat16, 141), randn((4, 617), torch.bfloat16, 142)
+    w = randn((617,), torch.float32, 143)
+
+    def step():
+        gx, dw = sgc.disco_rms_norm_bwd(x, w, gy, axis=-1)
+        outs = [torch.empty_like(gx), torch.empty_like(dw)]
+        return [gx, dw, sgc.disco_grad_norm([gx, dw]), sgc.disco_clip_grads([gx, dw], 0.5, out=outs), *outs]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for k in range(4):
+        x.copy_(randn(x.shape, torch.bfloat16, 150 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), f"replay {k}"
+
+
+@pytest.mark.parametrize("sizes", [[16384], [16385], [8192, 8192], [8193, 8191], [2000] * 8, [2000] * 9, [1] * 8, [1] * 9], ids=str)
+def test_clip_at_the_border_of_one_workgroup(sizes):
+    print(f"[clip] {sizes}", flush=True)
+    grads = [randn((n,), torch.float32, 160 + i, 0.5) for i, n in enumerate(sizes)]  # apart from each other
+    ref = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    factor = min(1.0, 0.125 / (ref + EPS))
+    whole = torch.empty(sum(sizes), device=DEV)
+    for outs in (list(whole.split(sizes)), [torch.empty_like(g) for g in grads]):
+        n = sgc.disco_clip_grads(grads, 0.125, out=outs)
+        assert float(n) == float(sgc.disco_grad_norm(grads)) and abs(float(n) - ref) <= 2 * U * ref
+        for g, o in zip(grads, outs):
+            r = g.double() * factor
+            close(o, r, r.abs() * (half(g.dtype) + 4 * U) * 1.001 + 1e-40, "out")
+
+
 def test_offsets_beyond_32_bits():
     # 3 x (2^30 + 72) points of bf16: byte offsets pass 2^32 and element offsets 2^31
     M = (1 << 30) + 72
