@@ -55,7 +55,7 @@ struct GradTensor {
 };
 
 constexpr int kGradBatch = 120;     // runs a launch takes in its arguments (32 bytes each, below 4 KiB; 128 at most)
-constexpr int kGradBlocks = 2048;   // workgroups of one norm launch, so partial sums it leaves
+constexpr int kGradBlocks = 2048;   // workgroups of one norm launch (all a GPU holds), so partial sums it leaves
 constexpr int kGradDirect = 2048;   // up to so many partial sums, each scaling workgroup adds them itself
 
 struct GradBatch {

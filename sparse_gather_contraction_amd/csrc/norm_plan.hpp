@@ -134,7 +134,10 @@ inline NormGeom norm_geom(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
         const bool flat = M < kColsMinM;
         g.vec = flat ? 1 : vmax;
         // Channels a thread, then as many lanes along the points as the workgroup has threads for: a run of
-        // 64 lanes x 16 bytes of each channel at most.
+        // 64 lanes x 16 bytes of each channel at most.  Longer runs cost memory less: forward, 2x256x721x1440 bf16,
+        // 8 channels and 32 lanes 836 us, 8 and 16 860, 4 and 16 858; 8 bits, 1x80x721x1440, 8 and 64 126, 8 and 32 129,
+        // 8 and 16 138.  Backward (two inputs, so half the channels fit), 2x64x361x720, 4 and 32 46.6, 4 and 16 49.6,
+        // 2 and 32 52.8.
         g.per = D >= 16 && !bwd ? 8 : D >= 8 ? 4 : D >= 4 ? 2 : 1;
         const int64_t ng = ceil_div64(D, g.per);
         int lg = bwd && esz == 2 && !flat ? 5 : 6;  // the backward's LDS holds two sums a point
