@@ -125,12 +125,13 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
             for (int e = 0; e < VEC; ++e) atomicMax(&mx[k * P + lane * VEC + e], abs_bits(m[e]));
         __syncthreads();
         if (c0 >= a.D) return;
-        float s[VEC], mul[VEC];
+        float s[VEC], inv[VEC], back[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const F8Scale f = f8_scale(__uint_as_float(mx[k * P + lane * VEC + e]), a.qmax);
             s[e] = f.scale;
-            mul[e] = f.mul;
+            inv[e] = f.inv;
+            back[e] = f.back;
         }
         if (c0 == k * a.group) store_f32<float, VEC>(a.scale + (pos.n * a.ngroups + k) * a.M + pos.m, s);
         uint8_t *q = (uint8_t *)a.y + base;
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_cols_kernel(NormArgs a)
             if (c0 + j < a.D) {
                 float v[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = h[j][e] * mul[e];
+                for (int e = 0; e < VEC; ++e) v[e] = f8_quot(h[j][e], inv[e], back[e]);
                 Pack<uint8_t, VEC> pq;
                 pack_f8(v, a.f8, pq);
                 store_pack<uint8_t, VEC, NT>(q + (int64_t)(c0 + j) * a.M, pq);
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_rows_kernel(NormArgs a)
             if (c == grp * a.group) a.scale[row * a.ngroups + grp] = f.scale;
             float v[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = h[k][e] * f.mul;
+            for (int e = 0; e < VEC; ++e) v[e] = f8_quot(h[k][e], f.inv, f.back);
             Pack<uint8_t, VEC> pq;
             pack_f8(v, a.f8, pq);
             store_own<uint8_t, VEC, NT>(q + pos[k].c, pq, pos[k].dup);
@@ -367,7 +368,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void norm_loop_kernel(NormArgs a)
             for (int c = lo + g; c < hi; c += groups) {
                 const float v = value(c);
                 if constexpr (RES) store_elem((T *)a.h + base, (int64_t)c * a.M, v);
-                const float q1[1] = {v * rstd * load_weight<T>(a.w, a.wf32, c) * f.mul};
+                const float q1[1] = {f8_quot(v * rstd * load_weight<T>(a.w, a.wf32, c), f.inv, f.back)};
                 Pack<uint8_t, 1> pq;
                 pack_f8(q1, a.f8, pq);
                 store_pack<uint8_t, 1>((uint8_t *)a.y + base + (int64_t)c * a.M, pq);

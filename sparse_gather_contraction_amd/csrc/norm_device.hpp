@@ -331,20 +331,30 @@ __device__ __forceinline__ float join_apart(float v, int lg, Op op)
     return v;
 }
 
-// The scale of a group whose largest |y| is amax (0 or more), and the factor that takes y to its quotient.
-//   scale = amax / qmax, at least 2^-126 (the reciprocal of a smaller one leaves fp32's range); mul = qmax / amax,
-// which is 1 / scale without scale's own rounding, so y mul is off by one rounding each of the quotient and the
-// product, as y / scale is.  amax infinite: scale infinite and mul 0, so a finite y gives 0 and an infinite one
-// NaN; amax NaN: both NaN.
+// The scale of a group whose largest |y| is amax (0 or more) and what takes its values to their quotients.
+//   scale = amax / qmax, at least 2^-126 (the reciprocal of a smaller one leaves fp32's range).
+// A quotient is y / scale by the scale as it is stored, which the reader multiplies by: the product with the
+// reciprocal (off by 2^-23 at most), then its remainder y - q scale brought in, two fma an element.  That is off by
+// 2^-45 before its one rounding to fp32; the product alone, off by the reciprocal's error too, sent values next to
+// a tie to the other code.
+// amax infinite: scale infinite, a finite y gives 0 and an infinite one NaN (inv and back are 0: with the
+// infinite scale itself the remainder of a finite y would be NaN); amax NaN: all NaN.
 struct F8Scale {
-    float scale, mul;
+    float scale, inv, back;
 };
 
 __device__ __forceinline__ F8Scale f8_scale(float amax, float qmax)
 {
     const float s = amax / qmax;
-    if (s < 0x1p-126f) return {0x1p-126f, 0x1p126f};
-    return {s, qmax / amax};
+    if (s < 0x1p-126f) return {0x1p-126f, 0x1p126f, 0x1p-126f};
+    const float inv = __builtin_amdgcn_rcpf(s);
+    return {s, inv, inv == 0.0f ? 0.0f : s};
+}
+
+__device__ __forceinline__ float f8_quot(float y, float inv, float back)
+{
+    const float q = y * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, back, y), inv, q);
 }
 
 }  // namespace disco

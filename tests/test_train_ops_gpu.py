@@ -489,3 +489,32 @@ def test_offsets_beyond_32_bits():
     n = float(sgc.disco_grad_norm([x]))
     ref = math.sqrt(sum(float(x[0, i, j:j + (1 << 28)].double().square().sum()) for i in range(3) for j in range(0, M, 1 << 28)))
     assert abs(n - ref) <= 2 * U * ref
+
+
+# Rows in registers with one group, groups joined over lanes and through LDS, several vectors a thread, single
+# elements; columns, flat tiles; the looping kernels.
+QUOTIENTS = [((300, 512), -1, 128), ((300, 512), -1, 0), ((99, 1000), -1, 96), ((40, 4100), -1, 64), ((1029, 7), -1, 0), ((3, 70001), -1, 128),
+             ((2, 80, 13, 41), 1, 0), ((1, 257, 9, 43), 1, 32), ((64, 66, 3), 1, 32), ((1, 2500, 5, 13), 1, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", QUOTIENTS, ids=lambda v: ids(v) + f"g{v[2]}")
+def test_f8_codes_are_the_quotients_by_the_stored_scale(case, dtype):
+    # Whole numbers up to 8 (e4m3) and 14 (e5m2) with weights of 1: the sums of squares are exact in any order, so the
+    # fp32 norm of the same numbers gives the y that the 8-bit form rounds, and multiples of 448 / 8 and 57344 / 14 are
+    # often half way between two codes, where the last bit of y / scale decides.  The quotient is rounded once to fp32
+    # and that once to 8 bits.
+    shape, axis, group = case
+    for f8, top in (("e4m3", 8), ("e5m2", 14)):
+        print(f"[quotients] {shape} axis {axis} group {group} {dtype} {f8}", flush=True)
+        qt, qmax = F8[f8][0], F8[f8][1]
+        gen = torch.Generator().manual_seed(171)
+        x = torch.randint(-top, top + 1, shape, generator=gen).to(T[dtype]).to(DEV)
+        w = torch.ones(shape[axis], device=DEV)
+        y = sgc.disco_rms_norm(x.float(), w, axis=axis, eps=EPS).cpu()
+        q, scale = (t.cpu() for t in sgc.disco_rms_norm_f8(x, w, axis=axis, eps=EPS, group=group, dtype=qt))
+        g = group or shape[axis]
+        for k, ys in enumerate(y.split(g, axis)):
+            s = (ys.abs().amax(axis, keepdim=True) / qmax).clamp(min=2.0 ** -126)
+            assert torch.equal(scale.narrow(axis, k, 1), s)
+            assert torch.equal(q.narrow(axis, k * g, ys.shape[axis]).float(), (ys / s).to(qt).float())
