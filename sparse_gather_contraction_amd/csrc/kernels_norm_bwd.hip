@@ -9,8 +9,8 @@
 // Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
 // registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
 // registers over the workgroup's tiles (a vector's terms in fp32, the vectors in fp64), then over its lanes, and
-// the workgroups' partial rows are summed in fp64 by a second launch; every order is fixed, so results are bitwise
-// reproducible.
+// the workgroups' partial rows are summed in fp64 by a second launch.  Rows too long for that have dw summed by a
+// launch of its own (dw_rows_kernel).  Every order is fixed, so results are bitwise reproducible.
 //
 // Memory bounds it: 2x256x721x1440 bf16 with gh 781-856 us from card to card (5.0-5.4 TB/s; a copy in the same
 // 256-byte runs takes 815-930), 259200x512 bf16 193 us (5.5 TB/s), 4x32x181x360 fp32 21.7 us and 3.9 of the second launch.
@@ -25,8 +25,9 @@ namespace {
 struct BwdArgs {
     const void *h, *gy, *gh, *w;
     void *gx;
-    float *partial;
-    void *dw;      // not null: the launch is one workgroup, whose sums are dw itself
+    part_t *partial;
+    float *rstd;   // long rows: rstd of each row, for the launch that sums dw
+    void *dw;      // not null: the sums of the launch's one workgroup, or one chunk of rows, are dw itself
     int64_t N, M, tiles;
     int32_t D, wf32, lg, tiles_n;
     float eps;
@@ -40,11 +41,11 @@ __device__ __forceinline__ int fresh(int v)
     return v;
 }
 
-// A workgroup's sum for channel c: its entry of the partial sums, or dw.
+// The sum for channel c of workgroup or chunk `part`: its entry of the partial sums, or dw.
 template <typename T>
-__device__ __forceinline__ void store_dw(const BwdArgs &a, int c, double s)
+__device__ __forceinline__ void store_dw(const BwdArgs &a, int part, int c, double s)
 {
-    if (!a.dw) a.partial[(int64_t)blockIdx.x * a.D + c] = (float)s;
+    if (!a.dw) a.partial[(int64_t)part * a.D + c] = s;
     else if (a.wf32) ((float *)a.dw)[c] = (float)s;
     else store_elem((T *)a.dw, c, (float)s);
 }
@@ -186,21 +187,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     for (int c = t; c < a.D; c += blockDim.x) {
         double s = lds[c];
         for (int i = 1; i < waves; ++i) s += (double)lds[i * width + c];
-        store_dw<T>(a, c, s);
+        store_dw<T>(a, blockIdx.x, c, s);
     }
 }
 
 struct Sum2 {
     float u, v;
-};
-
-template <bool C, typename A, typename B>
-struct If {
-    typedef A type;
-};
-template <typename A, typename B>
-struct If<false, A, B> {
-    typedef B type;
 };
 
 // Two sums over the 2^lg threads of a row.
@@ -222,7 +214,11 @@ __device__ __forceinline__ Sum2 row_sum2(Sum2 s, int lg, Sum2 *slots)
     return s;
 }
 
-// Rows (M = 1).  Dynamic LDS: [rows][D] for the join of dw where a workgroup holds several rows.
+// Rows (M = 1).  dw is summed here, but for four vectors of 16 bits a thread: they do not have the registers for fp64
+// sums and keep each row's rstd for dw_rows_kernel.
+// Dynamic LDS: [rows][D] for the join of dw where a workgroup holds several rows; four vectors of fp32 a thread keep
+// the weights of the first three there, each thread its own, in the place of registers that the sums of dw take
+// (20000x10000 fp32 597 against 707 us, 16000x16384 778 against 840).
 template <typename T, int VEC, int KPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 {
@@ -231,25 +227,44 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
     const int t = threadIdx.x, lanes = 1 << a.lg, tt = t & (lanes - 1), slot = t >> a.lg;
     const int rows = blockDim.x >> a.lg;
     RowPos pos[KPT];
-    // dw of a thread's elements over its rows, in fp64 where registers are left (up to two vectors a thread)
-    using Acc = typename If<KPT <= 2, double, float>::type;
-    float w[KPT][VEC];
-    Acc acc[KPT][VEC];
+    constexpr bool DW = KPT * VEC <= 16;
+    constexpr int LW = KPT == 4 && VEC == 4 ? kBwdLdsWeights : 0;
+    float w[KPT - LW][VEC];
+    f32x4 *const lw = (f32x4 *)lds + t;
+    auto weight = [&](int k, float (&f)[VEC]) {
+        if constexpr (LW > 0)
+            if (k < LW) {
+                const f32x4 v = lw[k * blockDim.x];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = v[e];
+                return;
+            }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = w[k - LW][e];
+    };
+    double acc[KPT][VEC];
 #pragma unroll
     for (int k = 0; k < KPT; ++k) {
         pos[k] = row_pos(k * lanes + tt, VEC, a.D);
-        if (a.wf32) load_f32<float, VEC>((const float *)a.w + pos[k].c, w[k]);
-        else load_f32<T, VEC>((const T *)a.w + pos[k].c, w[k]);
+        float f[VEC];
+        if (a.wf32) load_f32<float, VEC>((const float *)a.w + pos[k].c, f);
+        else load_f32<T, VEC>((const T *)a.w + pos[k].c, f);
+        if constexpr (LW > 0)
+            if (k < LW) lw[k * blockDim.x] = f32x4{f[0], f[1], f[2], f[3]};
+        if (k >= LW)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[k - LW][e] = f[e];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[k][e] = 0;
     }
     Pack<T, VEC> ph[KPT], pg[KPT], pr[KPT];
     bool live = false;
-    int64_t base = 0;
+    int64_t row = 0, base = 0;
     auto load_tile = [&](int64_t tile) {
         const int64_t want = tile * rows + slot;
         live = want < a.N;
-        base = (live ? want : a.N - 1) * a.D;  // a slot past the end repeats the last row
+        row = live ? want : a.N - 1;  // a slot past the end repeats the last row
+        base = row * a.D;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             ph[k] = load_pack<T, VEC>((const T *)a.h + base + pos[k].c);
@@ -265,18 +280,21 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         Sum2 s = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-            float h[VEC], gy[VEC];
+            float h[VEC], gy[VEC], wk[VEC];
             unpack(ph[k], h);
             unpack(pg[k], gy);
+            weight(k, wk);
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 if (e >= pos[k].dup) {
                     s.u = __builtin_fmaf(h[e], h[e], s.u);
-                    s.v = __builtin_fmaf(gy[e] * w[k][e], h[e], s.v);
+                    s.v = __builtin_fmaf(gy[e] * wk[e], h[e], s.v);
                 }
         }
         s = row_sum2(s, a.lg, slots);
         const float rstd = rsqrtf(s.u / (float)a.D + a.eps), c = rstd * (s.v / (float)a.D);
+        if constexpr (!DW)
+            if (tt == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             keep_packed(ph[k]);
@@ -284,14 +302,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         }
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-            float h[VEC], gy[VEC], o[VEC];
+            float h[VEC], gy[VEC], wk[VEC], o[VEC];
             unpack(ph[k], h);
             unpack(pg[k], gy);
+            weight(k, wk);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd;
-                acc[k][e] += live && e >= pos[k].dup ? (Acc)(gy[e] * u) : (Acc)0;
-                o[e] = rstd * (gy[e] * w[k][e] - u * c);
+                if constexpr (DW) acc[k][e] += live && e >= pos[k].dup ? (double)(gy[e] * u) : 0.0;
+                o[e] = rstd * (gy[e] * wk[e] - u * c);
             }
             if constexpr (RES) {
                 float r[VEC];
@@ -301,8 +320,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
             }
             pack(o, pr[k]);
             keep_here(pr[k]);
+            if constexpr (DW)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) keep_here(acc[k][e]);
+                for (int e = 0; e < VEC; ++e) keep_here(acc[k][e]);
         }
         T *gx = (T *)a.gx + base;
         if (tile + gridDim.x < a.tiles) load_tile(tile + gridDim.x);  // before this row's stores, as in columns
@@ -310,6 +330,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         for (int k = 0; k < KPT; ++k)
             if (pos[k].dup < VEC) store_pack<T, VEC, NT>(gx + pos[k].c, pr[k]);
     }
+    if constexpr (!DW) return;
     if (rows > 1) {
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
@@ -320,26 +341,68 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
         for (int c = t; c < a.D; c += blockDim.x) {
             double s = 0.0;
             for (int i = 0; i < rows; ++i) s += (double)lds[i * a.D + c];
-            store_dw<T>(a, c, s);
+            store_dw<T>(a, blockIdx.x, c, s);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= pos[k].dup) store_dw<T>(a, pos[k].c + e, (double)acc[k][e]);
+                if (e >= pos[k].dup) store_dw<T>(a, blockIdx.x, pos[k].c + e, acc[k][e]);
     }
 }
 
-// More channels than registers hold: the threads walk the channels twice, and the workgroup's row of
-// partial sums is kept in device memory, each entry by one thread.
+// dw of long rows, in a launch of its own: a thread holds the fp64 sums of one vector of columns over a chunk of
+// rows and reads h and gy once more.  Memory bounds it.  fp64 sums beside gx take more registers than there are (with
+// fp32 ones, 20000x20000 bf16 took 1246 us with 216 bytes a thread spilled, both launches here 884), and a row of sums
+// for each workgroup in device memory costs a read and a write of 8 bytes an element (2000x40000 bf16 620 us, here 455;
+// the looping kernel with fp32 sums there 537).
+template <typename T>
+__global__ __launch_bounds__(kDwThreads) void dw_rows_kernel(BwdArgs a, int64_t rows)
+{
+    constexpr int VEC = 16 / (int)sizeof(T), U = 4;
+    const int v = blockIdx.x * kDwThreads + threadIdx.x;
+    if ((int64_t)v * VEC >= a.D) return;
+    const RowPos pos = row_pos(v, VEC, a.D);
+    const int64_t lo = blockIdx.y * rows, hi = lo + rows < a.N ? lo + rows : a.N;
+    const T *hp = (const T *)a.h + pos.c, *gp = (const T *)a.gy + pos.c;
+    double acc[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.0;
+    for (int64_t i = lo; i < hi; i += U) {
+        Pack<T, VEC> ph[U], pg[U];
+        float rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i + u < hi ? i + u : hi - 1;
+            ph[u] = load_pack<T, VEC>(hp + row * a.D);
+            pg[u] = load_pack<T, VEC>(gp + row * a.D);
+            rstd[u] = a.rstd[row];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < hi) {
+                float h[VEC], gy[VEC];
+                unpack(ph[u], h);
+                unpack(pg[u], gy);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[e] += (double)(gy[e] * (h[e] * rstd[u]));
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        if (e >= pos.dup) store_dw<T>(a, blockIdx.y, pos.c + e, acc[e]);
+}
+
+// More channels than registers hold: the threads walk the channels twice.  Rows leave dw to dw_rows_kernel; else a
+// workgroup's row of partial sums is kept in device memory, each entry by one thread.
 template <typename T, bool RES>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
 {
     extern __shared__ float lds[];
     const int t = threadIdx.x, P = 1 << a.lg, lane = t & (P - 1), g = t >> a.lg, groups = blockDim.x >> a.lg;
     float *s_hh = lds, *s_gh = lds + groups * P;
-    float *mine = a.partial + (int64_t)blockIdx.x * a.D;
+    part_t *mine = a.partial + (int64_t)blockIdx.x * a.D;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         const ColPos pos = col_pos(tile, lane, 1, a.lg, 0, a.N, a.M);
         const int64_t base = pos.n * a.D * a.M + pos.m;
@@ -363,33 +426,35 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
         }
         const float rstd = rsqrtf(s_hh[lane] / (float)a.D + a.eps);
         const float k = rstd * (s_gh[lane] / (float)a.D);
+        if (a.rstd && t == 0) a.rstd[tile] = rstd;
         for (int c = g; c < a.D; c += groups) {
             const float h = load_elem(hp, (int64_t)c * a.M), gy = load_elem(gp, (int64_t)c * a.M);
             const float u = h * rstd;
             float o = rstd * (gy * load_weight<T>(a.w, a.wf32, c) - u * k);
             if constexpr (RES) o += load_elem((const T *)a.gh + base, (int64_t)c * a.M);
             store_elem((T *)a.gx + base, (int64_t)c * a.M, o);
+            if (a.rstd) continue;  // uniform
             float d = pos.dup ? 0.0f : gy * u;
             for (int i = 1; i < P; i <<= 1) d += __shfl_xor(d, i);  // P <= 64 lanes of one wave walk together
-            if (lane == 0) mine[c] = tile == blockIdx.x ? d : mine[c] + d;
+            if (lane == 0) mine[c] = tile == blockIdx.x ? (double)d : mine[c] + (double)d;
         }
     }
 }
 
 // dw[c] = the sum of partial[0..blocks)[c]: 16 columns a workgroup, 64 threads a column, fp64.
 template <typename O>
-__global__ __launch_bounds__(1024) void dw_sum_kernel(const float *partial, int blocks, int D, O *dw)
+__global__ __launch_bounds__(1024) void dw_sum_kernel(const part_t *partial, int blocks, int D, O *dw)
 {
     __shared__ double part[16][16];
     const int col = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
     double s = 0.0;
     if (c < D) {
         for (int i = r0; i < blocks; i += 8 * 64) {
-            float v[8];
+            double v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = i + u * 64 < blocks ? partial[(int64_t)(i + u * 64) * D + c] : 0.0f;
+            for (int u = 0; u < 8; ++u) v[u] = i + u * 64 < blocks ? partial[(int64_t)(i + u * 64) * D + c] : 0.0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += (double)v[u];
+            for (int u = 0; u < 8; ++u) s += v[u];
         }
     }
     s += __shfl_xor(s, 16);
@@ -448,49 +513,38 @@ hipError_t launch_t(const BwdArgs &a, const NormGeom &g, int blocks, hipStream_t
 }
 
 template <typename T>
-hipError_t launch_r(const BwdArgs &a, const NormGeom &g, bool res, int blocks, hipStream_t s)
+hipError_t launch_r(BwdArgs a, const BwdPlan &p, bool res, void *dw, hipStream_t s)
 {
-    return res ? launch_t<T, true>(a, g, blocks, s) : launch_t<T, false>(a, g, blocks, s);
+    const hipError_t e = res ? launch_t<T, true>(a, p.g, p.blocks, s) : launch_t<T, false>(a, p.g, p.blocks, s);
+    if (e != hipSuccess || !p.apart) return e;
+    a.dw = p.parts == 1 ? dw : nullptr;
+    dw_rows_kernel<T><<<dim3((uint32_t)p.dw_tiles, (uint32_t)p.parts), kDwThreads, 0, s>>>(a, p.dw_rows);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-// Up to two tiles are done by one workgroup, which then needs no second launch (4x617 bf16 6.4 against 10.0 us).
-static bool one_block(const NormGeom &g) { return !g.loop && g.tiles <= 2; }
-
-// 256 CUs; 1024 threads of these kernels' registers a CU, and half of them for rows: fewer rows open at a time
-// (259200x512 bf16 194 against 214 us, fp32 389 against 433 us).
-int32_t norm_bwd_blocks(int64_t N, int64_t D, int64_t M, int esz)
-{
-    if (N == 0 || M == 0) return 0;
-    const NormGeom g = norm_geom(N, D, M, esz, true);
-    if (one_block(g)) return 1;
-    const int each = g.rows ? 512 : 1024;
-    const int64_t most = 256 * (g.threads >= each ? 1 : each / g.threads);
-    return (int32_t)(g.tiles < most ? g.tiles : most);
-}
-
 hipError_t launch_norm_bwd(const NormLaunch &l, hipStream_t s)
 {
-    const int esz = l.dtype == 0 ? 4 : 2;
-    if (l.blocks > 0) {
-        const NormGeom g = norm_geom(l.N, l.D, l.M, esz, true);
-        const bool one = one_block(g);
+    const BwdPlan p = norm_bwd_plan(l.N, l.D, l.M, l.dtype == 0 ? 4 : 2);
+    part_t *partial = (part_t *)l.workspace;
+    if (p.blocks > 0) {
         BwdArgs a;
-        a.dw = one ? l.dw : nullptr;
-        a.h = l.x; a.gy = l.gy; a.gh = l.r; a.w = l.w; a.gx = l.y; a.partial = l.partial;
-        a.N = l.N; a.M = l.M; a.tiles = g.tiles;
-        a.D = (int32_t)l.D; a.wf32 = l.wf32; a.lg = g.lg; a.tiles_n = g.tiles_n; a.eps = l.eps;
+        a.dw = !p.apart && p.direct() ? l.dw : nullptr;
+        a.h = l.x; a.gy = l.gy; a.gh = l.r; a.w = l.w; a.gx = l.y; a.partial = partial;
+        a.rstd = p.apart ? (float *)(partial + (int64_t)p.parts * l.D) : nullptr;
+        a.N = l.N; a.M = l.M; a.tiles = p.g.tiles;
+        a.D = (int32_t)l.D; a.wf32 = l.wf32; a.lg = p.g.lg; a.tiles_n = p.g.tiles_n; a.eps = l.eps;
         const bool res = l.r != nullptr;
-        const hipError_t e = l.dtype == 0 ? launch_r<float>(a, g, res, l.blocks, s)
-                           : l.dtype == 1 ? launch_r<bf16_t>(a, g, res, l.blocks, s)
-                                          : launch_r<f16_t>(a, g, res, l.blocks, s);
-        if (e != hipSuccess || one) return e;
+        const hipError_t e = l.dtype == 0 ? launch_r<float>(a, p, res, l.dw, s)
+                           : l.dtype == 1 ? launch_r<bf16_t>(a, p, res, l.dw, s)
+                                          : launch_r<f16_t>(a, p, res, l.dw, s);
+        if (e != hipSuccess || p.direct()) return e;
     }
     const dim3 grid((uint32_t)ceil_div64(l.D, 16));
-    if (l.wf32) dw_sum_kernel<float><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (float *)l.dw);
-    else if (l.dtype == 1) dw_sum_kernel<bf16_t><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (bf16_t *)l.dw);
-    else dw_sum_kernel<f16_t><<<grid, 1024, 0, s>>>(l.partial, l.blocks, (int)l.D, (f16_t *)l.dw);
+    if (l.wf32) dw_sum_kernel<float><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (float *)l.dw);
+    else if (l.dtype == 1) dw_sum_kernel<bf16_t><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (bf16_t *)l.dw);
+    else dw_sum_kernel<f16_t><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (f16_t *)l.dw);
     return hipGetLastError();
 }
 

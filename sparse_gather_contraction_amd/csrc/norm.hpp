@@ -8,6 +8,8 @@
 
 namespace disco {
 
+typedef double part_t __attribute__((aligned(4)));   // a partial sum of dw: a workspace has fp32's alignment
+
 // element types: 0 = fp32, 1 = bf16, 2 = fp16
 struct NormLaunch {
     const void *x = nullptr;   // forward: x; backward: the stored sum h
@@ -18,7 +20,7 @@ struct NormLaunch {
     void *h = nullptr;         // forward: the stored sum (with r)
     float *scale = nullptr;    // 8-bit output
     void *dw = nullptr;        // backward
-    float *partial = nullptr;  // backward: [blocks][D]
+    void *workspace = nullptr; // backward: as BwdPlan::bytes says
     int32_t dtype = 0;
     int32_t wf32 = 1;          // the weight (and dw) is fp32, else of the data type
     int64_t N = 0, D = 0, M = 0;
@@ -26,13 +28,10 @@ struct NormLaunch {
     int32_t f8 = -1;           // -1: no 8-bit output, 0: e4m3, 1: e5m2
     int32_t group = 0;         // channels of one scale (8-bit output)
     int32_t ngroups = 1;
-    int32_t blocks = 0;        // backward: workgroups (rows of `partial`)
 };
 
 hipError_t launch_norm(const NormLaunch &a, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormLaunch &a, hipStream_t stream);
-// Workgroups of the backward, and so rows of its workspace of blocks * D floats.
-int32_t norm_bwd_blocks(int64_t N, int64_t D, int64_t M, int esz);
 
 struct DequantLaunch {
     const uint8_t *q;

@@ -525,7 +525,7 @@ disco_status disco_rms_norm_bwd_workspace(const disco_tensor *h, int axis, size_
         View v;
         const disco_status st = view_of(h, "h", axis, &v);
         if (st != DISCO_OK) return st;
-        *bytes = (size_t)disco::norm_bwd_blocks(v.N, v.D, v.M, (int)elem_size(h->dtype)) * (size_t)v.D * sizeof(float);
+        *bytes = disco::norm_bwd_plan(v.N, v.D, v.M, (int)elem_size(h->dtype)).bytes(v.N, v.D);
         return DISCO_OK;
     });
 }
@@ -550,15 +550,14 @@ disco_status disco_rms_norm_bwd(const disco_tensor *h, const disco_tensor *w, co
         if (gh && (st = same_shape(gh, "gh", h, v.axis, v.D)) != DISCO_OK) return st;
         if (!(eps >= 0.0f) || std::isinf(eps))
             return api_fail(DISCO_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
-        const int esz = (int)elem_size(h->dtype);
-        const int32_t blocks = disco::norm_bwd_blocks(v.N, v.D, v.M, esz);
-        const size_t need = (size_t)blocks * (size_t)v.D * sizeof(float);
+        const disco::BwdPlan plan = disco::norm_bwd_plan(v.N, v.D, v.M, (int)elem_size(h->dtype));
+        const size_t need = plan.bytes(v.N, v.D);
         int dev = -1;
         if ((st = current_device(&dev)) != DISCO_OK) return st;
         if ((st = check_pointer(dw->data, "dw", dev)) != DISCO_OK) return st;
         Range ins[4] = {range_of(h, "h"), range_of(w, "w"), range_of(gy, "gy")}, outs[3] = {range_of(gx, "gx"), range_of(dw, "dw")};
         int ni = 3;
-        if (blocks > 0) {  // without points only dw is written, as zeros
+        if (plan.blocks > 0) {  // without points only dw is written, as zeros
             if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 3))
                 return api_fail(DISCO_ERR_INVALID_ARGUMENT, "workspace is NULL, not 4-byte aligned or too small");
             if ((st = check_pointer(h->data, "h", dev)) != DISCO_OK) return st;
@@ -573,9 +572,9 @@ disco_status disco_rms_norm_bwd(const disco_tensor *h, const disco_tensor *w, co
         }
         disco::NormLaunch a;
         a.x = h->data; a.r = gh ? gh->data : nullptr; a.gy = gy->data; a.w = w->data;
-        a.y = gx->data; a.dw = dw->data; a.partial = (float *)workspace;
+        a.y = gx->data; a.dw = dw->data; a.workspace = workspace;
         a.dtype = h->dtype; a.wf32 = w->dtype == DISCO_F32;
-        a.N = v.N; a.D = v.D; a.M = v.M; a.eps = eps; a.blocks = blocks;
+        a.N = v.N; a.D = v.D; a.M = v.M; a.eps = eps;
         return launched(disco::launch_norm_bwd(a, (hipStream_t)stream), "norm backward");
     });
 }

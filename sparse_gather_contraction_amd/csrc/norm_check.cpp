@@ -75,6 +75,40 @@ static void check_norm(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
     for (int h : held) REQUIRE(h == 1);
 }
 
+// The backward's launches: every tile is taken once, a workgroup's partial sums lie inside the workspace, and the
+// launch that sums dw of long rows adds every element once to one entry of its chunk.
+static void check_bwd_plan(int64_t N, int64_t D, int64_t M, int esz)
+{
+    const BwdPlan p = norm_bwd_plan(N, D, M, esz);
+    REQUIRE(p.blocks >= 1 && p.blocks <= p.g.tiles && p.parts >= 1);
+    std::vector<int> taken((size_t)p.g.tiles, 0);
+    for (int64_t b = 0; b < p.blocks; ++b)
+        for (int64_t i = b; i < p.g.tiles; i += p.blocks) ++taken[(size_t)i];
+    for (int t : taken) REQUIRE(t == 1);
+    REQUIRE(p.bytes(N, D) >= (size_t)p.parts * D * 8 + (p.apart ? N * 4 : 0));
+    if (!p.apart) {
+        REQUIRE(p.parts == p.blocks);
+        REQUIRE(!p.g.rows || p.g.per * p.g.vec <= 16);  // rows that sum dw in registers
+        return;
+    }
+    REQUIRE(M == 1 && D >= 16 / esz);
+    const int V = 16 / esz;
+    std::vector<int> cols((size_t)D, 0), rows((size_t)N, 0);
+    for (int64_t v = 0; v < p.dw_tiles * kDwThreads; ++v) {
+        if (v * V >= D) continue;
+        const RowPos q = row_pos((int)v, V, (int)D);
+        REQUIRE(q.dup >= 0 && q.dup < V && q.c >= 0 && q.c + V <= D);
+        for (int e = q.dup; e < V; ++e) ++cols[(size_t)(q.c + e)];
+    }
+    for (int64_t k = 0; k < p.parts; ++k) {
+        const int64_t lo = k * p.dw_rows, hi = lo + p.dw_rows < N ? lo + p.dw_rows : N;
+        REQUIRE(lo < hi);
+        for (int64_t r = lo; r < hi; ++r) ++rows[(size_t)r];
+    }
+    for (int c : cols) REQUIRE(c == 1);
+    for (int r : rows) REQUIRE(r == 1);
+}
+
 static void check_dequant(int64_t N, int64_t D, int64_t M, int esz)
 {
     const DequantGeom g = dequant_geom(N, D, M, esz);
@@ -130,9 +164,13 @@ int main()
                     check_norm(N, D, M, esz, false);
                     check_norm(N, D, M, esz, true);
                     check_dequant(N, D, M, esz);
-                    done += 3;
+                    check_bwd_plan(N, D, M, esz);
+                    done += 4;
                 }
             }
+    for (int64_t N : {9, 32, 33, 255, 256, 257, 2000, 40001})  // long rows: no walk over the elements
+        for (int64_t D : {8192, 8193, 16385, 20000, 32769, 40000, 1 << 20})
+            for (int esz = 2; esz <= 4; esz += 2, ++done) check_bwd_plan(N, D, 1, esz);
     printf("%lld geometries checked\n", (long long)done);
     return 0;
 }

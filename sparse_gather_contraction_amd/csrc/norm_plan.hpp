@@ -187,14 +187,58 @@ inline size_t norm_lds(const NormGeom &g, int ngroups)
     return (size_t)(cols_parts(g) + 1 + ngroups) * P * 4;
 }
 
+constexpr int kBwdLdsWeights = 3;   // rows, four vectors of fp32 a thread: vectors whose weights lie in LDS
+
 inline size_t norm_bwd_lds(const NormGeom &g, int64_t D)
 {
     const size_t P = ((size_t)1 << g.lg) * g.vec;
     if (g.loop) return 2 * g.groups * P * 4;
+    if (g.rows && g.per == 4 && g.vec == 4) return (size_t)kBwdLdsWeights * g.threads * 16;
     if (g.rows) return g.groups > 1 ? (size_t)g.groups * D * 4 : 0;
     const size_t join = (size_t)(2 * cols_parts(g) + 2) * P * 4;
     const size_t last = (size_t)(g.lg > 6 ? 1 << (g.lg - 6) : 1) * g.groups * g.per * 4;
     return join > last ? join : last;
+}
+
+// ---- the backward's launches
+
+constexpr int kDwThreads = 256;
+
+struct BwdPlan {
+    NormGeom g;
+    int32_t blocks = 0;    // workgroups of the first launch, each walking every blocks-th tile
+    bool apart = false;    // long rows: dw is summed by a launch of its own
+    int32_t parts = 0;     // rows of D partial sums of dw: one a workgroup, or one a chunk of rows
+    int64_t dw_tiles = 0, dw_rows = 0;  // long rows: workgroups along the row, rows of a chunk
+    // dw is written without a launch that adds the parts
+    bool direct() const { return parts == 1 && (apart || !g.loop); }
+    // [parts][D] fp64, then (long rows) [N] fp32 of rstd
+    size_t bytes(int64_t N, int64_t D) const { return (size_t)parts * (size_t)D * 8 + (apart ? (size_t)N * 4 : 0); }
+};
+
+inline BwdPlan norm_bwd_plan(int64_t N, int64_t D, int64_t M, int esz)
+{
+    BwdPlan p;
+    if (N == 0 || M == 0) return p;
+    p.g = norm_geom(N, D, M, esz, true);
+    p.apart = M == 1 && (p.g.loop || (p.g.per == 4 && esz == 2));
+    // Up to two tiles are done by one workgroup, which then needs no second launch (4x617 bf16 6.4 against 10.0 us).
+    const bool one = !p.g.loop && !p.apart && p.g.tiles <= 2;
+    // 256 CUs; 1024 threads of these kernels' registers a CU, and half of them for rows: fewer rows open at a time
+    // (259200x512 bf16 194 against 214 us, fp32 389 against 433 us).
+    const int each = p.g.rows ? 512 : 1024;
+    const int64_t most = one ? 1 : 256 * (p.g.threads >= each ? 1 : each / p.g.threads);
+    p.blocks = (int32_t)(p.g.tiles < most ? p.g.tiles : most);
+    p.parts = p.blocks;
+    if (p.apart) {
+        // Up to 32 rows are one chunk, which needs no third launch (9x40000 bf16 23.8 against 29.5 us); more are as many
+        // chunks of 8 rows or more as 8 workgroups a CU take (40x20000 bf16 16.4 us, chunks of 32 or more 18.5).
+        p.dw_tiles = ceil_div64(D, (int64_t)kDwThreads * (16 / esz));
+        const int64_t want = p.dw_tiles < 2048 ? 2048 / p.dw_tiles : 1, most_parts = N <= 32 ? 1 : ceil_div64(N, 8);
+        p.dw_rows = ceil_div64(N, want < most_parts ? want : most_parts);
+        p.parts = (int32_t)ceil_div64(N, p.dw_rows);
+    }
+    return p;
 }
 
 // ---- reader of the 8-bit form

@@ -200,3 +200,11 @@ def checker(tmp_path_factory):
 def test_every_access_of_the_norm_kernels_lies_inside(checker):
     r = subprocess.run([checker], capture_output=True, text=True)
     assert r.returncode == 0 and "geometries checked" in r.stdout, r.stdout + r.stderr
+
+
+def test_the_workspace_of_long_rows_stays_small():
+    lib, n = sgc.load_library(), ctypes.c_size_t()
+    for rows, D in ((100000, 1 << 20), (5000, 40000), (40000, 20000), (33, 1 << 26)):
+        assert lib.disco_rms_norm_bwd_workspace(desc((rows, D)), 1, n) == 0
+        # fp64 sums of dw for the chunks of rows that fill the GPU (2048 x 256 threads of 8 columns, or one row), rstd
+        assert D * 8 <= n.value <= max(2048 * 256 * 8, D) * 8 + rows * 4, (rows, D, n.value)

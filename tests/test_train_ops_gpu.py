@@ -518,3 +518,61 @@ def test_f8_codes_are_the_quotients_by_the_stored_scale(case, dtype):
             s = (ys.abs().amax(axis, keepdim=True) / qmax).clamp(min=2.0 ** -126)
             assert torch.equal(scale.narrow(axis, k, 1), s)
             assert torch.equal(q.narrow(axis, k * g, ys.shape[axis]).float(), (ys / s).to(qt).float())
+
+
+# dw over many rows of long axes: rows in registers with four vectors a thread (fp32 and 16 bits), the looping kernel
+# with more tiles than workgroups and a last round that is not full, over rows and over columns.
+LONG = [((2500, 16390), -1), ((9, 20000), -1), ((3000, 20011), -1), ((700, 8201), -1), ((600, 32776), -1), ((1, 1040, 96, 97), 1)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", LONG, ids=ids)
+def test_dw_of_long_axes(case, dtype):
+    # Against the formula, and in a workspace of NaN and one of large values: nothing of it may be taken over.
+    shape, axis = case
+    print(f"[long dw] {shape} axis {axis} {dtype}", flush=True)
+    dt = T[dtype]
+    gen = torch.Generator(device=DEV).manual_seed(181)
+    h, gy, gh = (torch.randn(shape, generator=gen, device=DEV).to(dt) for _ in range(3))
+    w = randn((shape[axis],), torch.float32, 182)
+    need = sgc.disco_rms_norm_bwd_workspace(h, axis=axis)
+    first = None
+    for fill in (255, 0x7e):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        got = sgc.disco_rms_norm_bwd(h, w, gy, gh=gh, axis=axis, eps=EPS, workspace=ws)
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, got))
+        first = got
+    gx, dw = first
+    total = torch.zeros(shape[axis], dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(total)
+    cut = 0 if axis == -1 else 2  # in pieces: the fp64 intermediates are large
+    for lo in range(0, shape[cut], -(-shape[cut] // 8)):
+        k = min(-(-shape[cut] // 8), shape[cut] - lo)
+        H, GY, GH, GX = (t.narrow(cut, lo, k) for t in (h, gy, gh, gx))
+        ref, bound, rdw, sdw = bwd_reference(H, w, GY, GH, axis)
+        close(GX, ref, ref.abs() * half(dt) * 1.001 + bound + 1e-40, "gx")
+        total += rdw
+        size += sdw
+    # each term 44 u; joins of 32 points at most in fp32, then fp64
+    close(dw, total, total.abs() * U * 1.001 + 50 * U * size + 1e-40, "dw")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", [((15616, 16390), -1), ((15616, 9000), -1), ((15616, 20000), -1), ((1, 1040, 704, 710), 1)], ids=ids)
+def test_dw_of_long_axes_keeps_small_terms(case, dtype):
+    # |h| = 1, so rstd is one number r just below 1 and every term is r gy.  A large term in the first tile of each of
+    # 256 workgroups, then 60 small ones, each 3/8 of a step of the large one: an fp32 sum over the tiles drops them all
+    # (22 u), fp64 keeps them.  r is off by 3 u (mean 1 u, root 2 u), a term by 1 u more, the sum of a vector's or a
+    # wave's equal terms by nothing (powers of two of them), the result is rounded once: 5 u.
+    shape, axis = case
+    print(f"[small terms] {shape} axis {axis} {dtype}", flush=True)
+    dt = T[dtype]
+    D = shape[axis]
+    points, many, big, small = math.prod(shape) // D, 8192 if axis == 1 else 256, 2.0 ** 12, 1.5 * 2.0 ** -14
+    h = torch.ones(shape, dtype=dt, device=DEV)
+    gy = torch.full(shape, small, dtype=dt, device=DEV)
+    (gy.view(D, -1)[:, :many] if axis == 1 else gy[:many])[:] = big
+    _, dw = sgc.disco_rms_norm_bwd(h, torch.ones(D, device=DEV), gy, axis=axis, eps=EPS)
+    ref = (many * big + (points - many) * small) / math.sqrt(1 + EPS)
+    worst = float((dw.double() / ref - 1).abs().max())
+    assert worst <= 5 * U, worst / U
