@@ -8,7 +8,7 @@
 //
 // Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
 // registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
-// registers over the workgroup's tiles (a vector's terms in fp32, the vectors in fp64), then over its lanes, and
+// registers over the workgroup's tiles (each term rounded to fp32, their sum in fp64), then over its lanes, and
 // the workgroups' partial rows are summed in fp64 by a second launch.  Rows too long for that have dw summed by a
 // launch of its own (dw_rows_kernel).  Every order is fixed, so results are bitwise reproducible.
 //
@@ -51,11 +51,11 @@ __device__ __forceinline__ void store_dw(const BwdArgs &a, int part, int c, doub
 }
 
 // Columns (M > 1): the forward's tiles.  LDS: [parts][P] sums of h^2, [parts][P] of g h, [P] rstd,
-// [P] c; at the end [waves of one g][channels] of dw.
+// [P] c; at the end [waves of one g][channels] fp64 of dw.
 template <typename T, int VEC, int CPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 {
-    extern __shared__ float lds[];
+    extern __shared__ __attribute__((aligned(16))) float lds[];
     const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg;
     const int P = VEC << a.lg, groups = blockDim.x >> a.lg;
     const int lg6 = a.lg < 6 ? 6 : a.lg, parts = blockDim.x >> lg6, part = t >> lg6;
@@ -148,16 +148,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
         }
 #pragma unroll
         for (int j = 0; j < CPT; ++j) {
-            float h[VEC], gy[VEC], o[VEC], d = 0.0f;
+            float h[VEC], gy[VEC], o[VEC];
             unpack(ph[j], h);
             unpack(pg[j], gy);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd[e];
-                d = e >= pos.dup ? __builtin_fmaf(gy[e], u, d) : d;
+                acc[j] += e >= pos.dup ? (double)(gy[e] * u) : 0.0;
                 o[e] = rstd[e] * (gy[e] * w[j] - u * c[e]);
             }
-            acc[j] += (double)d;
             if constexpr (RES) {
                 float r[VEC];
                 unpack(pr[j], r);
@@ -179,14 +178,15 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
     const int in_wave = a.lg < 6 ? a.lg : 6, waves = a.lg > 6 ? 1 << (a.lg - 6) : 1, width = groups * CPT;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) acc[j] = join_run(acc[j], in_wave, AddOp());
+    double *sum = (double *)lds;
     __syncthreads();
     if ((lane & ((1 << in_wave) - 1)) == 0)
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) lds[(lane >> 6) * width + c0 + j] = (float)acc[j];
+        for (int j = 0; j < CPT; ++j) sum[(lane >> 6) * width + c0 + j] = acc[j];
     __syncthreads();
     for (int c = t; c < a.D; c += blockDim.x) {
-        double s = lds[c];
-        for (int i = 1; i < waves; ++i) s += (double)lds[i * width + c];
+        double s = sum[c];
+        for (int i = 1; i < waves; ++i) s += sum[i * width + c];
         store_dw<T>(a, blockIdx.x, c, s);
     }
 }
@@ -216,13 +216,13 @@ __device__ __forceinline__ Sum2 row_sum2(Sum2 s, int lg, Sum2 *slots)
 
 // Rows (M = 1).  dw is summed here, but for four vectors of 16 bits a thread: they do not have the registers for fp64
 // sums and keep each row's rstd for dw_rows_kernel.
-// Dynamic LDS: [rows][D] for the join of dw where a workgroup holds several rows; four vectors of fp32 a thread keep
+// Dynamic LDS: [rows][D] fp64 for the join of dw where a workgroup holds several rows; four vectors of fp32 a thread keep
 // the weights of the first three there, each thread its own, in the place of registers that the sums of dw take
 // (20000x10000 fp32 597 against 707 us, 16000x16384 778 against 840).
 template <typename T, int VEC, int KPT, bool RES, bool NT>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 {
-    extern __shared__ float lds[];
+    extern __shared__ __attribute__((aligned(16))) float lds[];
     __shared__ Sum2 slots[kNormMaxThreads / 64];
     const int t = threadIdx.x, lanes = 1 << a.lg, tt = t & (lanes - 1), slot = t >> a.lg;
     const int rows = blockDim.x >> a.lg;
@@ -332,15 +332,16 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
     }
     if constexpr (!DW) return;
     if (rows > 1) {
+        double *sum = (double *)lds;
 #pragma unroll
         for (int k = 0; k < KPT; ++k)
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= pos[k].dup) lds[slot * a.D + pos[k].c + e] = (float)acc[k][e];
+                if (e >= pos[k].dup) sum[slot * a.D + pos[k].c + e] = acc[k][e];
         __syncthreads();
         for (int c = t; c < a.D; c += blockDim.x) {
             double s = 0.0;
-            for (int i = 0; i < rows; ++i) s += (double)lds[i * a.D + c];
+            for (int i = 0; i < rows; ++i) s += sum[i * a.D + c];
             store_dw<T>(a, blockIdx.x, c, s);
         }
     } else {
@@ -399,7 +400,7 @@ __global__ __launch_bounds__(kDwThreads) void dw_rows_kernel(BwdArgs a, int64_t 
 template <typename T, bool RES>
 __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
 {
-    extern __shared__ float lds[];
+    extern __shared__ __attribute__((aligned(16))) float lds[];
     const int t = threadIdx.x, P = 1 << a.lg, lane = t & (P - 1), g = t >> a.lg, groups = blockDim.x >> a.lg;
     float *s_hh = lds, *s_gh = lds + groups * P;
     part_t *mine = a.partial + (int64_t)blockIdx.x * a.D;
@@ -434,9 +435,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
             if constexpr (RES) o += load_elem((const T *)a.gh + base, (int64_t)c * a.M);
             store_elem((T *)a.gx + base, (int64_t)c * a.M, o);
             if (a.rstd) continue;  // uniform
-            float d = pos.dup ? 0.0f : gy * u;
-            for (int i = 1; i < P; i <<= 1) d += __shfl_xor(d, i);  // P <= 64 lanes of one wave walk together
-            if (lane == 0) mine[c] = tile == blockIdx.x ? (double)d : mine[c] + (double)d;
+            // P <= 64 lanes of one wave walk together
+            const double d = join_run(pos.dup ? 0.0 : (double)(gy * u), a.lg, AddOp());
+            if (lane == 0) mine[c] = tile == blockIdx.x ? d : mine[c] + d;
         }
     }
 }

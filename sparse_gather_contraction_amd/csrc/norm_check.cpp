@@ -37,12 +37,15 @@ static void check_norm(int64_t N, int64_t D, int64_t M, int esz, bool bwd)
         if (g.loop) {
             REQUIRE((g.groups & (g.groups - 1)) == 0 && lanes <= 64);
             REQUIRE(lds >= (bwd ? 2 : 1) * (size_t)g.groups * P * 4 + (bwd ? 0 : P * 4));
-        } else if (!g.rows) {
+        } else if (g.rows) {
+            if (bwd && g.groups > 1) REQUIRE(lds >= (size_t)g.groups * D * 8);
+            if (bwd && g.groups == 1 && g.per == 4 && g.vec == 4) REQUIRE(lds >= (size_t)kBwdLdsWeights * g.threads * 16);
+        } else {
             const int lg6 = g.lg < 6 ? 6 : g.lg, parts = g.threads >> lg6;
             REQUIRE(parts * (1 << lg6) == g.threads);
             REQUIRE(lds >= (bwd ? (2 * (size_t)parts + 2) : (size_t)parts + 1 + ng) * P * 4);
             // dw: leader lanes write [lane >> 6][g * per + j]
-            if (bwd) REQUIRE(lds >= ((size_t)((lanes - 1) >> 6) * g.groups * g.per + (size_t)g.groups * g.per) * 4);
+            if (bwd) REQUIRE(lds >= ((size_t)((lanes - 1) >> 6) * g.groups * g.per + (size_t)g.groups * g.per) * 8);
             REQUIRE((int64_t)g.groups * g.per >= D && 32 % g.per == 0);
         }
     }

@@ -194,9 +194,9 @@ inline size_t norm_bwd_lds(const NormGeom &g, int64_t D)
     const size_t P = ((size_t)1 << g.lg) * g.vec;
     if (g.loop) return 2 * g.groups * P * 4;
     if (g.rows && g.per == 4 && g.vec == 4) return (size_t)kBwdLdsWeights * g.threads * 16;
-    if (g.rows) return g.groups > 1 ? (size_t)g.groups * D * 4 : 0;
+    if (g.rows) return g.groups > 1 ? (size_t)g.groups * D * 8 : 0;
     const size_t join = (size_t)(2 * cols_parts(g) + 2) * P * 4;
-    const size_t last = (size_t)(g.lg > 6 ? 1 << (g.lg - 6) : 1) * g.groups * g.per * 4;
+    const size_t last = (size_t)(g.lg > 6 ? 1 << (g.lg - 6) : 1) * g.groups * g.per * 8;
     return join > last ? join : last;
 }
 

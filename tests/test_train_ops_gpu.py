@@ -553,7 +553,7 @@ def test_dw_of_long_axes(case, dtype):
         close(GX, ref, ref.abs() * half(dt) * 1.001 + bound + 1e-40, "gx")
         total += rdw
         size += sdw
-    # each term 44 u; joins of 32 points at most in fp32, then fp64
+    # each term 44 u, summed in fp64
     close(dw, total, total.abs() * U * 1.001 + 50 * U * size + 1e-40, "dw")
 
 
@@ -574,5 +574,33 @@ def test_dw_of_long_axes_keeps_small_terms(case, dtype):
     (gy.view(D, -1)[:, :many] if axis == 1 else gy[:many])[:] = big
     _, dw = sgc.disco_rms_norm_bwd(h, torch.ones(D, device=DEV), gy, axis=axis, eps=EPS)
     ref = (many * big + (points - many) * small) / math.sqrt(1 + EPS)
+    worst = float((dw.double() / ref - 1).abs().max())
+    assert worst <= 5 * U, worst / U
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("case", [((1, 64, 361, 720), 1), ((3, 73, 91, 181), 1), ((1, 300, 128, 129), 1), ((6000, 24, 3), 1), ((40960, 512), -1), ((4096, 1), -1),
+                                  ((4, 617), -1), ((512, 9000), -1), ((256, 40000), -1), ((1, 2050, 64, 128), 1), ((1, 2050, 64, 128), 1, 2)],
+                         ids=lambda v: ids(v) + "+" * (len(v) - 2))
+def test_dw_of_sums_that_cancel(case, dtype):
+    # |h| = 1, so every term is r gy with one number r: 2^12 and -2^12 in the first and third quarters of the points,
+    # 1.5 2^-14 in the others.  The large terms cancel, so dw is the small ones' sum if every sum on the way keeps them;
+    # rounded to fp32 anywhere (in a vector, over lanes, in a workgroup, between launches) it is off by the large ones'
+    # half steps.  With a stride of 2 every second point is small in the large quarters too (the looping kernel).  r is off
+    # by 3 u, a term by 1 u more, the result is rounded once.
+    shape, axis, step = case if len(case) == 3 else (*case, 1)
+    print(f"[cancel] {shape} axis {axis} {dtype}", flush=True)
+    dt = T[dtype]
+    D = shape[axis]
+    points = math.prod(shape) // D
+    quarter = points // 4 // 64 * 64 if points >= 256 else points // 4
+    small = 1.5 * 2.0 ** -14
+    gy = torch.full((points,), small, dtype=dt, device=DEV)
+    gy[:quarter:step] = 2.0 ** 12
+    gy[2 * quarter:3 * quarter:step] = -2.0 ** 12
+    many = int((gy == small).sum()) if dt == torch.float32 else points - 2 * len(range(0, quarter, step))
+    gy = gy.view([s for i, s in enumerate(shape) if i != axis % len(shape)]).unsqueeze(axis).expand(shape).contiguous()
+    _, dw = sgc.disco_rms_norm_bwd(torch.ones_like(gy), torch.ones(D, device=DEV), gy, axis=axis, eps=EPS)
+    ref = many * small / math.sqrt(1 + EPS)
     worst = float((dw.double() / ref - 1).abs().max())
     assert worst <= 5 * U, worst / U
