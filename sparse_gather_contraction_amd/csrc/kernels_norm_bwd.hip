@@ -442,31 +442,35 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
     }
 }
 
-// dw[c] = the sum of partial[0..blocks)[c]: 16 columns a workgroup, 64 threads a column, fp64.
+// dw[c] = the sum of partial[0..parts)[c]: 16 columns a workgroup at a time, 64 threads a column, fp64.
 template <typename O>
-__global__ __launch_bounds__(1024) void dw_sum_kernel(const part_t *partial, int blocks, int D, O *dw)
+__global__ __launch_bounds__(kDwSumThreads) void dw_sum_kernel(const part_t *partial, int parts, int D, O *dw)
 {
-    __shared__ double part[16][16];
-    const int col = threadIdx.x & 15, r0 = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
-    double s = 0.0;
-    if (c < D) {
-        for (int i = r0; i < blocks; i += 8 * 64) {
-            double v[8];
+    __shared__ double part[16][kDwSumCols];
+    const int col = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    for (int64_t c0 = (int64_t)blockIdx.x * kDwSumCols; c0 < D; c0 += (int64_t)gridDim.x * kDwSumCols) {
+        const int64_t c = c0 + col;
+        double s = 0.0;
+        if (c < D) {
+            for (int i = r0; i < parts; i += 8 * 64) {
+                double v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = i + u * 64 < blocks ? partial[(int64_t)(i + u * 64) * D + c] : 0.0;
+                for (int u = 0; u < 8; ++u) v[u] = i + u * 64 < parts ? partial[(int64_t)(i + u * 64) * D + c] : 0.0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += v[u];
+                for (int u = 0; u < 8; ++u) s += v[u];
+            }
         }
-    }
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if ((threadIdx.x & 63) < 16) part[threadIdx.x >> 6][col] = s;
-    __syncthreads();
-    if (r0 == 0 && c < D) {
-        s = part[0][col];
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if ((threadIdx.x & 63) < 16) part[threadIdx.x >> 6][col] = s;
+        __syncthreads();
+        if (r0 == 0 && c < D) {
+            s = part[0][col];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += part[i][col];
-        store_elem(dw, c, (float)s);
+            for (int i = 1; i < 16; ++i) s += part[i][col];
+            store_elem(dw, c, (float)s);
+        }
+        __syncthreads();
     }
 }
 
@@ -542,10 +546,10 @@ hipError_t launch_norm_bwd(const NormLaunch &l, hipStream_t s)
                                           : launch_r<f16_t>(a, p, res, l.dw, s);
         if (e != hipSuccess || p.direct()) return e;
     }
-    const dim3 grid((uint32_t)ceil_div64(l.D, 16));
-    if (l.wf32) dw_sum_kernel<float><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (float *)l.dw);
-    else if (l.dtype == 1) dw_sum_kernel<bf16_t><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (bf16_t *)l.dw);
-    else dw_sum_kernel<f16_t><<<grid, 1024, 0, s>>>(partial, p.parts, (int)l.D, (f16_t *)l.dw);
+    const dim3 grid((uint32_t)dw_sum_blocks(l.D));
+    if (l.wf32) dw_sum_kernel<float><<<grid, kDwSumThreads, 0, s>>>(partial, p.parts, (int)l.D, (float *)l.dw);
+    else if (l.dtype == 1) dw_sum_kernel<bf16_t><<<grid, kDwSumThreads, 0, s>>>(partial, p.parts, (int)l.D, (bf16_t *)l.dw);
+    else dw_sum_kernel<f16_t><<<grid, kDwSumThreads, 0, s>>>(partial, p.parts, (int)l.D, (f16_t *)l.dw);
     return hipGetLastError();
 }
 

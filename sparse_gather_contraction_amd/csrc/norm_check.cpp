@@ -112,6 +112,20 @@ static void check_bwd_plan(int64_t N, int64_t D, int64_t M, int esz)
     for (int r : rows) REQUIRE(r == 1);
 }
 
+// The launch that adds the parts of dw fits a launch, and its walk takes every column once.
+static void check_dw_sum(int64_t D, bool walk)
+{
+    const int64_t N = 0, M = 0, blocks = dw_sum_blocks(D);
+    const int esz = 8;
+    REQUIRE(blocks >= 1 && blocks * kDwSumThreads <= (int64_t)UINT32_MAX);
+    if (!walk) return;
+    std::vector<int> taken((size_t)D, 0);
+    for (int64_t b = 0; b < blocks; ++b)
+        for (int64_t c0 = b * kDwSumCols; c0 < D; c0 += blocks * kDwSumCols)
+            for (int64_t c = c0; c < c0 + kDwSumCols && c < D; ++c) ++taken[(size_t)c];
+    for (int t : taken) REQUIRE(t == 1);
+}
+
 static void check_dequant(int64_t N, int64_t D, int64_t M, int esz)
 {
     const DequantGeom g = dequant_geom(N, D, M, esz);
@@ -159,6 +173,8 @@ int main()
     const int64_t Ms[] = {1, 2, 3, 7, 8, 15, 63, 64, 65, 127, 128, 129, 255, 1000, 1303};
     const int64_t Ns[] = {1, 2, 3, 5, 67, 300};
     int64_t done = 0;
+    for (int64_t D : {1, 16, 17, 1 << 20, (1 << 20) + 77, 1 << 23}) check_dw_sum(D, true), ++done;
+    for (int64_t D : {(1 << 26) - 15, 1 << 26, 1 << 30}) check_dw_sum(D, false), ++done;
     for (int64_t D : Ds)
         for (int64_t M : Ms)
             for (int64_t N : Ns) {

@@ -241,6 +241,15 @@ inline BwdPlan norm_bwd_plan(int64_t N, int64_t D, int64_t M, int esz)
     return p;
 }
 
+constexpr int kDwSumThreads = 1024, kDwSumCols = 16;
+
+// Workgroups of the launch that adds the parts of dw; longer axes are walked.
+inline int64_t dw_sum_blocks(int64_t D)
+{
+    const int64_t all = ceil_div64(D, kDwSumCols);
+    return all < (1 << 16) ? all : 1 << 16;
+}
+
 // ---- reader of the 8-bit form
 
 constexpr int kDequantCpt = 8;   // columns: channels a thread

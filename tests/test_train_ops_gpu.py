@@ -604,3 +604,26 @@ def test_dw_of_sums_that_cancel(case, dtype):
     ref = many * small / math.sqrt(1 + EPS)
     worst = float((dw.double() / ref - 1).abs().max())
     assert worst <= 5 * U, worst / U
+
+
+def test_dw_of_very_long_axes():
+    # 2^26 columns and more: 16 a workgroup of 1024 threads are more threads than a launch has
+    D = (1 << 26) + 3
+    e, w = torch.empty((0, D), dtype=torch.bfloat16, device=DEV), torch.ones(D, device=DEV)
+    dw = torch.full((D,), float("nan"), device=DEV)
+    sgc.disco_rms_norm_bwd(e, w, e, axis=1, dw=dw)
+    assert bool((dw == 0).all())
+    shape = (1, (1 << 20) + 77, 2)  # more columns than that launch's workgroups take at once
+    h, gy = randn(shape, torch.bfloat16, 191), randn(shape, torch.bfloat16, 192)
+    w = randn((shape[1],), torch.float32, 193)
+    gx, dw = sgc.disco_rms_norm_bwd(h, w, gy, axis=1, eps=EPS)
+    # chains of 2^20 / 32 terms and a tree of 32 in the sums over the axis: 32773 u of their terms' sizes; the root half
+    # of that, and the bounds of test_norm_bwd follow with 16387 and 32775 in the place of 40 and 82
+    H, G = h.double(), gy.double() * per(w.double(), h, 1)
+    rstd = (H.square().mean(1, keepdim=True) + EPS).rsqrt()
+    mean, size = (G * H).mean(1, keepdim=True), (G * H).abs().mean(1, keepdim=True)
+    a, b = rstd * G, H * rstd ** 3 * mean
+    bound = U * (16396 * a.abs() + 49170 * b.abs() + 32780 * H.abs() * rstd ** 3 * size)
+    close(gx, a - b, (a - b).abs() * half(torch.bfloat16) * 1.001 + bound + 1e-40, "gx")
+    terms = gy.double() * H * rstd
+    close(dw, terms.sum((0, 2)), U * (1 + 16396) * terms.abs().sum((0, 2)) + 1e-40, "dw")
