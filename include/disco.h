@@ -264,8 +264,9 @@ disco_status disco_grad_norm(int64_t n, const disco_tensor *grads, disco_tensor 
 
 /* Clipping by that norm: outs[i] = grads[i] * min(1, max_norm / (norm + eps)), each rounded once; norm is the
  * norm before clipping.  outs[i] has the shape and dtype of grads[i] and is either the same memory (in place;
- * nothing is rewritten where the factor is 1) or disjoint from everything else.  A NaN norm makes every
- * output NaN, an infinite one makes finite elements 0.  The factor stays on the device. */
+ * nothing is rewritten where the factor is 1) or disjoint from everything else.  max_norm may be infinite (no
+ * limit).  Where norm + eps and max_norm are both 0 the factor is 1.  A NaN gradient makes every output NaN, an infinite
+ * one makes finite elements 0 and infinite ones NaN, whatever max_norm is.  The factor stays on the device. */
 disco_status disco_clip_grads(int64_t n, const disco_tensor *grads, float max_norm, float eps, disco_tensor *outs,
                               disco_tensor *norm, void *workspace, size_t workspace_bytes, void *stream);
 

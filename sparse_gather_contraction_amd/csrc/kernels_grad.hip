@@ -168,11 +168,13 @@ __device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, i
     else scale_chunk<T, false>(p, o, n, k, threadIdx.x);
 }
 
-// The factor of a total norm; a NaN norm gives NaN.
+// The factor of a total norm: min(1, max_norm / (total + eps)), 1 where both are 0 (nothing to clip) and 0 for an
+// infinite norm whatever max_norm is; a NaN norm gives NaN.
 __device__ __forceinline__ float clip_factor(double total, float max_norm, float eps)
 {
-    const double c = (double)max_norm / (total + (double)eps);
-    return (float)(c >= 1.0 ? 1.0 : c);
+    const double t = total + (double)eps;
+    if (__builtin_isinf(t)) return 0.0f;
+    return (double)max_norm >= t ? 1.0f : (float)((double)max_norm / t);
 }
 
 // Few elements: one workgroup sums all chunks and scales them, kThreads threads a chunk.

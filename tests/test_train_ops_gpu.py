@@ -627,3 +627,32 @@ def test_dw_of_very_long_axes():
     close(gx, a - b, (a - b).abs() * half(torch.bfloat16) * 1.001 + bound + 1e-40, "gx")
     terms = gy.double() * H * rstd
     close(dw, terms.sum((0, 2)), U * (1 + 16396) * terms.abs().sum((0, 2)) + 1e-40, "dw")
+
+
+@pytest.mark.parametrize("n", [5, 70000])
+def test_clip_factor_at_its_limits(n):
+    print(f"[clip] limits of {n}", flush=True)
+    inf, nan = float("inf"), float("nan")
+
+    def clip(values, max_norm, eps=EPS):
+        g = torch.ones(n, device=DEV) * values[0]
+        g[3] = values[-1]
+        out = torch.full_like(g, 7.0)
+        norm = float(sgc.disco_clip_grads([g], max_norm, out=[out], eps=eps))
+        mine = g.clone()
+        sgc.disco_clip_grads([mine], max_norm, eps=eps)
+        assert torch.equal(mine.isnan(), out.isnan()) and torch.equal(mine[~mine.isnan()], out[~out.isnan()])
+        return norm, out
+
+    norm, out = clip([0.0], 0.0, eps=0.0)  # 0 / 0: there is nothing to clip
+    assert norm == 0 and bool((out == 0).all())
+    norm, out = clip([2.0], 0.0, eps=0.0)
+    assert bool((out == 0).all())
+    for max_norm in (1.0, inf, 1e300):  # an infinite norm makes finite elements 0, also where no limit is set
+        norm, out = clip([2.0, -inf], max_norm)
+        assert norm == inf and bool(out[3].isnan()) and bool((out[4:] == 0).all()) and bool((out[:3] == 0).all())
+    norm, out = clip([2.0], inf)
+    assert bool((out == 2).all())
+    for max_norm in (0.0, 1.0, inf):
+        norm, out = clip([2.0, nan], max_norm)
+        assert norm != norm and bool(out.isnan().all())
