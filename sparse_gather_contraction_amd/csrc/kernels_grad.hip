@@ -85,8 +85,8 @@ __device__ __forceinline__ double sum_squares(const T *p, int n, int t)
     return s0 + s1;
 }
 
-template <typename T, bool NT>
-__device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k, int t)
+template <typename T, bool NT, typename K>
+__device__ __forceinline__ void scale_by(const T *p, T *o, int n, K k, int t)
 {
     constexpr int V = 16 / (int)sizeof(T), S = kThreads * V;
     walk<T, NT>(p, n, t, [&](const Pack<T, V> (&r)[kUnroll], int i, bool full) {
@@ -96,12 +96,26 @@ __device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, float k, in
                 float f[V];
                 unpack(r[u], f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) f[e] *= k;
+                for (int e = 0; e < V; ++e) f[e] = (float)(f[e] * k);
                 store_f32<T, V, NT>(o + i + u * S, f);
             }
     });
     const int tail = n - n % V + t;
-    if (tail < n) store_elem(o, tail, load_elem(p, tail) * k);
+    if (tail < n) store_elem(o, tail, (float)(load_elem(p, tail) * k));
+}
+
+// The factor of the gradients, in fp32 and, where it lies below fp32's normal range, as it was computed: a subnormal
+// fp32 factor has few bits or none left where the products have all of theirs (gradients of 1e38 by 1e-43).
+struct Factor {
+    float k;
+    double c;   // 0: k is all there is to it
+};
+
+template <typename T, bool NT>
+__device__ __forceinline__ void scale_chunk(const T *p, T *o, int n, const Factor &k, int t)
+{
+    if (k.c == 0.0) scale_by<T, NT>(p, o, n, k.k, t);
+    else scale_by<T, false>(p, o, n, k.c, t);
 }
 
 // The sum of a value over the workgroup of THREADS, the same in every thread.
@@ -160,7 +174,7 @@ __global__ __launch_bounds__(kThreads) void grad_total_kernel(double *partial, i
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, int n, float k, bool nt)
+__device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, int n, const Factor &k, bool nt)
 {
     const T *p = (const T *)t.p + off;
     T *o = (T *)t.o + off;
@@ -170,11 +184,13 @@ __device__ __forceinline__ void scale_tensor(const GradTensor &t, int64_t off, i
 
 // The factor of a total norm: min(1, max_norm / (total + eps)), 1 where both are 0 (nothing to clip) and 0 for an
 // infinite norm whatever max_norm is; a NaN norm gives NaN.
-__device__ __forceinline__ float clip_factor(double total, float max_norm, float eps)
+__device__ __forceinline__ Factor clip_factor(double total, float max_norm, float eps)
 {
     const double t = total + (double)eps;
-    if (__builtin_isinf(t)) return 0.0f;
-    return (double)max_norm >= t ? 1.0f : (float)((double)max_norm / t);
+    if (__builtin_isinf(t)) return {0.0f, 0.0};
+    if ((double)max_norm >= t) return {1.0f, 0.0};
+    const double c = (double)max_norm / t;
+    return {(float)c, c < 0x1p-126 ? c : 0.0};
 }
 
 // Few elements: one workgroup sums all chunks and scales them, kThreads threads a chunk.
@@ -197,10 +213,10 @@ __global__ __launch_bounds__(1024) void grad_small_kernel(GradSmall g, GradSmall
         partial[0] = s;
         *norm = (float)total;
     }
-    const float k = clip_factor(total, max_norm, eps);
+    const Factor k = clip_factor(total, max_norm, eps);
     for (int i = first; i < out.count; i += step) {
         const GradTensor &v = out.t[i];
-        if (v.p == v.o && k == 1.0f) continue;  // in place and unchanged
+        if (v.p == v.o && k.k == 1.0f) continue;  // in place and unchanged
         switch (v.dtype) {
         case 0: scale_chunk<float, false>((const float *)v.p, (float *)v.o, (int)v.n, k, t); break;
         case 1: scale_chunk<bf16_t, false>((const bf16_t *)v.p, (bf16_t *)v.o, (int)v.n, k, t); break;
@@ -216,13 +232,13 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, const
     const Firsts firsts = load_firsts(b);
     const double total = sqrt(total_of(partial, n));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
-    const float k = clip_factor(total, max_norm, eps);
+    const Factor k = clip_factor(total, max_norm, eps);
     for (int id0 = blockIdx.x; id0 < b.chunks; id0 += gridDim.x) {
         const int id = b.chunks - 1 - id0;
         const GradTensor &t = b.t[find_tensor(firsts, id)];
         const int64_t off = (int64_t)(id - t.first) * b.chunk, left = t.n - off;
         const int len = (int)(left < b.chunk ? left : b.chunk);
-        if (t.p == t.o && k == 1.0f) continue;  // in place and unchanged
+        if (t.p == t.o && k.k == 1.0f) continue;  // in place and unchanged
         switch (t.dtype) {
         case 0: scale_tensor<float>(t, off, len, k, b.stream); break;
         case 1: scale_tensor<bf16_t>(t, off, len, k, b.stream); break;

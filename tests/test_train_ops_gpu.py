@@ -656,3 +656,19 @@ def test_clip_factor_at_its_limits(n):
     for max_norm in (0.0, 1.0, inf):
         norm, out = clip([2.0, nan], max_norm)
         assert norm != norm and bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [6, 70001])
+def test_clip_by_a_factor_below_the_normal_range(n, dtype):
+    # gradients of 1e37 by factors of 1e-40 and less: the products are ordinary numbers (but the last, which is below the
+    # normal range: half a subnormal step, 2^-150 in fp32 and 2^-134 in bf16).  The factor 3 u, the product 1.
+    print(f"[clip] tiny factors {n} {dtype}", flush=True)
+    g = (randn((n,), torch.float32, 201) * 1e37).to(T[dtype])
+    g[-1] = 1.5
+    total = float(g.double().square().sum().sqrt())
+    for max_norm in (1e-3, 1e-6, 1e-12):
+        ref = g.double() * (max_norm / (total + EPS))
+        for src, out in ((g, torch.empty_like(g)), 2 * (g.clone(),)):
+            sgc.disco_clip_grads([src], max_norm, out=[out])
+            close(out, ref, ref.abs() * (half(T[dtype]) + 4 * U) * 1.001 + (2.0 ** -150 if dtype == "f32" else 2.0 ** -134), "out")
