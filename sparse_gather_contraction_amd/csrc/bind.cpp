@@ -11,6 +11,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <string>
 #include <vector>
 
 #include "disco.h"
@@ -108,15 +109,19 @@ void *stream_of(const at::Tensor &t)
     return p;
 }
 
-void check(disco_status st)
+[[noreturn]] void raise_status(disco_status st, const char *message)
 {
-    if (st == DISCO_OK) return;
-    PyObject *e = PyObject_CallFunction(g_error, "is", (int)st, disco_last_error());
+    PyObject *e = PyObject_CallFunction(g_error, "is", (int)st, message);
     if (e) {
         PyErr_SetObject(g_error, e);
         Py_DECREF(e);
     }
     throw Raised();
+}
+
+void check(disco_status st)
+{
+    if (st != DISCO_OK) raise_status(st, disco_last_error());
 }
 
 // Runs a library call without the interpreter lock.
@@ -306,6 +311,9 @@ PyObject *grads_call(PyObject *list, PyObject *result, bool clip, float max_norm
             PyErr_SetString(PyExc_ValueError, "out must have one tensor for each gradient");
             throw Raised();
         }
+        for (int64_t i = 0; i < g.size(); ++i)  // the library sees them as their elements in a row
+            if (g[i].sizes() != o[i].sizes())
+                raise_status(DISCO_ERR_SHAPE, ("out[" + std::to_string(i) + "] does not have the shape of its gradient").c_str());
         call([&] { return disco_clip_grads(g.size(), g.d.data(), max_norm, eps, o.d.data(), &norm.d, ws.data_ptr(), need, s); });
     }
     return norm.out();

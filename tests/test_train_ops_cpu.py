@@ -208,3 +208,13 @@ def test_the_workspace_of_long_rows_stays_small():
         assert lib.disco_rms_norm_bwd_workspace(desc((rows, D)), 1, n) == 0
         # fp64 sums of dw for the chunks of rows that fill the GPU (2048 x 256 threads of 8 columns, or one row), rstd
         assert D * 8 <= n.value <= max(2048 * 256 * 8, D) * 8 + rows * 4, (rows, D, n.value)
+
+
+@pytest.mark.parametrize("shape", [(6, 4), (24,), (4, 6, 1), (1, 4, 6)], ids=str)
+def test_binding_refuses_outputs_of_another_shape(shape):
+    # as many elements, laid out otherwise: a gradient's transpose among them
+    a = torch.zeros((4, 6))
+    for grads, out in (([a], [torch.zeros(shape)]), ([a, a.clone()], [torch.zeros((4, 6)), torch.zeros(shape)])):
+        with pytest.raises(sgc.DiscoError) as e:
+            sgc.disco_clip_grads(grads, 1.0, out=out)
+        assert e.value.status_name == "DISCO_ERR_SHAPE" and f"out[{len(out) - 1}]" in str(e.value)
