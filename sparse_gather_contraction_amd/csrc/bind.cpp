@@ -249,39 +249,38 @@ PyObject *rms_norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// A sequence of tensors, held, each as its elements in a row.
+// A sequence of tensors, each held for the call and seen as its elements in a row.  The tensors are held themselves:
+// the sequence is the caller's, and another thread (or the code of another argument) may change it meanwhile.
 struct List {
-    PyObject *seq;
+    std::vector<at::Tensor> t;
     std::vector<disco_tensor> d;
-    explicit List(PyObject *o) : seq(PySequence_Fast(o, "expected a sequence of tensors"))
+    explicit List(PyObject *o)
     {
-        if (!seq) throw Raised();
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
-        d.resize((size_t)n);
-        for (Py_ssize_t i = 0; i < n; ++i) {
-            PyObject *e = PySequence_Fast_GET_ITEM(seq, i);
-            if (!THPVariable_Check(e)) {
-                PyErr_Format(PyExc_TypeError, "expected a tensor, got %s", Py_TYPE(e)->tp_name);
-                Py_DECREF(seq);
-                throw Raised();
-            }
-            const at::Tensor &t = THPVariable_Unpack(e);
-            if (!t.is_contiguous()) {
+        struct Ref {
+            PyObject *p;
+            ~Ref() { Py_XDECREF(p); }
+        } seq{PySequence_Fast(o, "expected a sequence of tensors")};
+        if (!seq.p) throw Raised();
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.p);
+        t.reserve((size_t)n);
+        d.reserve((size_t)n);
+        for (Py_ssize_t i = 0; i < n; ++i) {  // nothing in this loop runs Python code before it throws
+            const at::Tensor &v = tensor_of(PySequence_Fast_GET_ITEM(seq.p, i));
+            if (!v.is_contiguous()) {
                 PyErr_SetString(PyExc_ValueError, "disco tensors must be contiguous");
-                Py_DECREF(seq);
                 throw Raised();
             }
-            disco_tensor &v = d[(size_t)i];
-            v.data = t.data_ptr();
-            v.dtype = code_of(t.scalar_type());
-            v.ndim = 1;
-            v.shape[0] = t.numel();
+            disco_tensor e = {};
+            e.data = v.data_ptr();
+            e.dtype = code_of(v.scalar_type());
+            e.ndim = 1;
+            e.shape[0] = v.numel();
+            t.push_back(v);
+            d.push_back(e);
         }
     }
-    ~List() { Py_DECREF(seq); }
-    List(const List &) = delete;
-    int64_t size() const { return (int64_t)d.size(); }
-    const at::Tensor &operator[](size_t i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(seq, (Py_ssize_t)i)); }
+    int64_t size() const { return (int64_t)t.size(); }
+    const at::Tensor &operator[](int64_t i) const { return t[(size_t)i]; }
 };
 
 // grad_norm(grads, norm or None) and clip_grads(grads, max_norm, eps, out or None, norm or None): the result's

@@ -218,3 +218,22 @@ def test_binding_refuses_outputs_of_another_shape(shape):
         with pytest.raises(sgc.DiscoError) as e:
             sgc.disco_clip_grads(grads, 1.0, out=out)
         assert e.value.status_name == "DISCO_ERR_SHAPE" and f"out[{len(out) - 1}]" in str(e.value)
+
+
+def test_binding_holds_the_tensors_of_its_lists():
+    # `out` is walked after the gradients: what its walk does to the list of gradients must not free them
+    from torch.multiprocessing.reductions import StorageWeakRef
+
+    grads = [torch.zeros(1000 + i) for i in range(3)]
+    kept = [StorageWeakRef(g.untyped_storage()) for g in grads]
+    seen = []
+
+    class Out:
+        def __iter__(self):
+            grads.clear()
+            seen.extend(k.expired() for k in kept)
+            return iter([torch.zeros(1000 + i) for i in range(3)])
+
+    with pytest.raises(sgc.DiscoError):  # host memory
+        sgc.disco_clip_grads(grads, 1.0, out=Out())
+    assert seen == [False] * 3 and all(k.expired() for k in kept)
