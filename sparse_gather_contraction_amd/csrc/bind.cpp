@@ -249,38 +249,37 @@ PyObject *rms_norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// A sequence of tensors, each held for the call and seen as its elements in a row.  The tensors are held themselves:
-// the sequence is the caller's, and another thread (or the code of another argument) may change it meanwhile.
+// A sequence of tensors as a tuple of its own, which holds them for the call (the sequence is the caller's, and another
+// thread or the code of another argument may change it meanwhile), each seen as its elements in a row.
 struct List {
-    std::vector<at::Tensor> t;
+    PyObject *seq;
     std::vector<disco_tensor> d;
-    explicit List(PyObject *o)
+    explicit List(PyObject *o) : seq(PySequence_Tuple(o))
     {
-        struct Ref {
-            PyObject *p;
-            ~Ref() { Py_XDECREF(p); }
-        } seq{PySequence_Fast(o, "expected a sequence of tensors")};
-        if (!seq.p) throw Raised();
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.p);
-        t.reserve((size_t)n);
-        d.reserve((size_t)n);
-        for (Py_ssize_t i = 0; i < n; ++i) {  // nothing in this loop runs Python code before it throws
-            const at::Tensor &v = tensor_of(PySequence_Fast_GET_ITEM(seq.p, i));
-            if (!v.is_contiguous()) {
-                PyErr_SetString(PyExc_ValueError, "disco tensors must be contiguous");
-                throw Raised();
+        if (!seq) throw Raised();
+        try {
+            d.resize((size_t)PyTuple_GET_SIZE(seq));
+            for (int64_t i = 0; i < size(); ++i) {
+                const at::Tensor &t = tensor_of(PyTuple_GET_ITEM(seq, i));
+                if (!t.is_contiguous()) {
+                    PyErr_SetString(PyExc_ValueError, "disco tensors must be contiguous");
+                    throw Raised();
+                }
+                disco_tensor &v = d[(size_t)i];
+                v.data = t.data_ptr();
+                v.dtype = code_of(t.scalar_type());
+                v.ndim = 1;
+                v.shape[0] = t.numel();
             }
-            disco_tensor e = {};
-            e.data = v.data_ptr();
-            e.dtype = code_of(v.scalar_type());
-            e.ndim = 1;
-            e.shape[0] = v.numel();
-            t.push_back(v);
-            d.push_back(e);
+        } catch (...) {
+            Py_DECREF(seq);
+            throw;
         }
     }
-    int64_t size() const { return (int64_t)t.size(); }
-    const at::Tensor &operator[](int64_t i) const { return t[(size_t)i]; }
+    ~List() { Py_DECREF(seq); }
+    List(const List &) = delete;
+    int64_t size() const { return (int64_t)d.size(); }
+    const at::Tensor &operator[](int64_t i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(seq, i)); }
 };
 
 // grad_norm(grads, norm or None) and clip_grads(grads, max_norm, eps, out or None, norm or None): the result's
