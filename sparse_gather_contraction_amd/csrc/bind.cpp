@@ -11,6 +11,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -44,15 +45,25 @@ const at::Tensor &tensor_of(PyObject *o)
     return THPVariable_Unpack(o);
 }
 
+// A tensor that the caller holds was written: autograd's check of the tensors it saved sees that, as after any
+// operation in place.
+void wrote(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // An argument that may be None.
 struct Arg {
     at::Tensor t;
     disco_tensor d = {};
     bool given = false;
+    bool callers = false;   // else made here
     Arg() = default;
     explicit Arg(PyObject *o)
     {
-        if (o != Py_None) set(tensor_of(o));
+        if (o == Py_None) return;
+        set(tensor_of(o));
+        callers = true;
     }
     void set(const at::Tensor &v)
     {
@@ -68,8 +79,12 @@ struct Arg {
         for (int64_t i = 0; i < v.dim() && i < 5; ++i) d.shape[i] = v.size(i);
     }
     disco_tensor *ptr() { return given ? &d : nullptr; }
-    // The tensor handed back, after a call.
-    PyObject *out() const { return THPVariable_Wrap(t); }
+    // The tensor handed back, after a call that wrote it.
+    PyObject *out() const
+    {
+        if (callers) wrote(t);
+        return THPVariable_Wrap(t);
+    }
 };
 
 struct Required : Arg {
@@ -299,21 +314,27 @@ PyObject *grads_call(PyObject *list, PyObject *result, bool clip, float max_norm
     check(disco_grad_norm_workspace(g.size(), g.d.data(), &need));
     const at::Tensor ws = bytes_on(norm.t, need);
     void *s = stream_of(norm.t);
+    const List *written = nullptr;
+    std::optional<List> o;
     if (!clip) {
         call([&] { return disco_grad_norm(g.size(), g.d.data(), &norm.d, ws.data_ptr(), need, s); });
     } else if (into == Py_None) {
         call([&] { return disco_clip_grads(g.size(), g.d.data(), max_norm, eps, g.d.data(), &norm.d, ws.data_ptr(), need, s); });
+        written = &g;
     } else {
-        List o(into);
-        if (o.size() != g.size()) {
+        o.emplace(into);
+        if (o->size() != g.size()) {
             PyErr_SetString(PyExc_ValueError, "out must have one tensor for each gradient");
             throw Raised();
         }
         for (int64_t i = 0; i < g.size(); ++i)  // the library sees them as their elements in a row
-            if (g[i].sizes() != o[i].sizes())
+            if (g[i].sizes() != (*o)[i].sizes())
                 raise_status(DISCO_ERR_SHAPE, ("out[" + std::to_string(i) + "] does not have the shape of its gradient").c_str());
-        call([&] { return disco_clip_grads(g.size(), g.d.data(), max_norm, eps, o.d.data(), &norm.d, ws.data_ptr(), need, s); });
+        call([&] { return disco_clip_grads(g.size(), g.d.data(), max_norm, eps, o->d.data(), &norm.d, ws.data_ptr(), need, s); });
+        written = &*o;
     }
+    if (written)
+        for (int64_t i = 0; i < written->size(); ++i) wrote((*written)[i]);
     return norm.out();
 }
 

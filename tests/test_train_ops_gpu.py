@@ -672,3 +672,32 @@ def test_clip_by_a_factor_below_the_normal_range(n, dtype):
         for src, out in ((g, torch.empty_like(g)), 2 * (g.clone(),)):
             sgc.disco_clip_grads([src], max_norm, out=[out])
             close(out, ref, ref.abs() * (half(T[dtype]) + 4 * U) * 1.001 + (2.0 ** -150 if dtype == "f32" else 2.0 ** -134), "out")
+
+
+def test_written_tensors_count_as_changed_in_place():
+    x, w = randn((40, 64), torch.bfloat16, 211), randn((64,), torch.float32, 212)
+    e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device=DEV)
+    y, h, gx, dw = e(40, 64), e(40, 64), e(40, 64), e(64, dt=torch.float32)
+    q, scale, out = e(40, 64, dt=torch.float8_e4m3fn), e(40, 1, dt=torch.float32), e(40, 64)
+    versions = [t._version for t in (x, w, y, h, gx, dw, q, scale, out)]
+    sgc.disco_rms_norm(x, w, residual=x, axis=-1, y=y, h=h)
+    sgc.disco_rms_norm_f8(x, w, axis=-1, q=q, scale=scale)
+    sgc.disco_dequantize(q, scale, axis=-1, out=out)
+    sgc.disco_rms_norm_bwd(h, w, y, axis=-1, gx=gx, dw=dw)
+    assert [t._version for t in (x, w, y, h, gx, dw, q, scale, out)] == [v + (i >= 2) for i, v in enumerate(versions)]
+    sgc.disco_grad_norm([gx, dw])
+    outs = [torch.empty_like(gx), torch.empty_like(dw)]
+    before = [t._version for t in (gx, dw, *outs)]
+    sgc.disco_clip_grads([gx, dw], 1e-3, out=outs)
+    sgc.disco_clip_grads([gx], 1e-3)
+    assert [t._version for t in (gx, dw, *outs)] == [before[0] + 1, before[1], before[2] + 1, before[3] + 1]
+    leaf = torch.ones(64, device=DEV, requires_grad=True)
+    saved = torch.full((64,), 3.0, device=DEV)
+    loss = (leaf * saved).sum()
+    sgc.disco_clip_grads([saved], 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():  # tensors without a count
+        t = torch.full((64,), 3.0, device=DEV)
+    sgc.disco_clip_grads([t], 1e-3)
+    assert float(t[0]) < 1
