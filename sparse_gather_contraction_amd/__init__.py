@@ -339,15 +339,22 @@ def disco_rms_norm(x, w, residual=None, axis=1, eps=1e-6, y=None, h=None):
 def disco_rms_norm_f8(x, w, residual=None, axis=1, eps=1e-6, group=0, dtype=None, q=None, scale=None, h=None):
     """disco_rms_norm with its output in 8 bits: (q, scale), or (q, scale, h) with a residual.
 
-    q is of `dtype` (torch.float8_e4m3fn, the default, or torch.float8_e5m2); scale (fp32) has x's shape with the axis
-    replaced by the number of runs of `group` entries (0: one run, the whole axis; else a multiple of 32)."""
-    code = 0 if dtype is None or q is not None else _f8_code(dtype)
+    q is of `dtype` (torch.float8_e4m3fn, the default, or torch.float8_e5m2), which a given q must have too; scale (fp32)
+    has x's shape with the axis replaced by the number of runs of `group` entries (0: one run, the whole axis; else a
+    multiple of 32)."""
+    code = 0 if dtype is None else _f8_code(dtype, q)
     return (_bind or _binding()).rms_norm_f8(x, w, residual, axis, eps, group, code, q, scale, h)
 
 
-def _f8_code(dtype):
+def _given_of(dtype, given, name):
+    if given is not None and getattr(given, "dtype", dtype) != dtype:
+        raise DiscoError(3, f"{name} is given and not of the dtype asked for")
+
+
+def _f8_code(dtype, q):
     import torch
 
+    _given_of(dtype, q, "q")
     if dtype == torch.float8_e4m3fn:
         return 0
     if dtype == torch.float8_e5m2:
@@ -356,14 +363,15 @@ def _f8_code(dtype):
 
 
 def disco_dequantize(q, scale, dtype=None, axis=1, group=0, out=None):
-    """out = q * scale in `dtype` (default bf16): the reader of disco_rms_norm_f8's form."""
-    code = DISCO_BF16 if dtype is None or out is not None else _data_code(dtype)
+    """out = q * scale in `dtype` (default bf16, or the given out's): the reader of disco_rms_norm_f8's form."""
+    code = DISCO_BF16 if dtype is None else _data_code(dtype, out)
     return (_bind or _binding()).dequantize(q, scale, code, axis, group, out)
 
 
-def _data_code(dtype):
+def _data_code(dtype, out):
     import torch
 
+    _given_of(dtype, out, "out")
     code = {torch.float32: DISCO_F32, torch.bfloat16: DISCO_BF16, torch.float16: DISCO_F16}.get(dtype)
     if code is None:
         raise DiscoError(3, "out has an unsupported dtype")

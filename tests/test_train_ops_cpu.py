@@ -237,3 +237,14 @@ def test_binding_holds_the_tensors_of_its_lists():
     with pytest.raises(sgc.DiscoError):  # host memory
         sgc.disco_clip_grads(grads, 1.0, out=Out())
     assert seen == [False] * 3 and all(k.expired() for k in kept)
+
+
+def test_a_given_output_of_another_dtype_than_asked_for_is_refused():
+    a, w, s = torch.zeros((4, 6)), torch.ones(6), torch.ones((4, 1))
+    q = a.to(torch.float8_e4m3fn)
+    for call in (lambda: sgc.disco_rms_norm_f8(a, w, axis=1, dtype=torch.float8_e5m2, q=q),
+                 lambda: sgc.disco_dequantize(q, s, dtype=torch.float32, out=a.half()),
+                 lambda: sgc.disco_dequantize(q, s, dtype=torch.int8, out=a.to(torch.int8))):
+        with pytest.raises(sgc.DiscoError) as e:
+            call()
+        assert e.value.status_name == "DISCO_ERR_DTYPE", e.value
