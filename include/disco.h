@@ -214,7 +214,8 @@ disco_status disco_fused_conv_bwd_noalloc(disco_psi h, const disco_tensor *x, co
  * (DISCO_ERR_INVALID_ARGUMENT).  All statistics are fp32 or wider, each output is rounded once (RNE), and
  * results are bitwise reproducible run to run.  Nothing is allocated on the device, so every call can be
  * captured into a graph.  A tensor with no elements is accepted and nothing is launched for it.
- * Squares are fp32 sums: a row whose sum of squares passes fp32's range (|h| near 2^64 / sqrt(D)) has rstd 0. */
+ * Squares are fp32 sums: a row whose sum of squares passes fp32's range (|h| near 2^64 / sqrt(D)) has rstd 0, and
+ * squares of |h| below 2^-75 are 0, so with eps = 0 a row of nothing else has an infinite rstd. */
 
 /* Root-mean-square norm over `axis`, of x or, with `residual`, of h = x + residual:
  *   y = h * rstd * w,   rstd = (mean(h^2) + eps)^(-1/2)

@@ -168,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void grad_total_kernel(double *partial, i
 {
     const double s = total_of(partial, n);
     if (threadIdx.x == 0) {
-        if (n > 0) partial[0] = s;
+        partial[0] = s;
         if (norm) *norm = (float)sqrt(s);
     }
 }
