@@ -8,7 +8,7 @@
 //
 // Each element of h, gy and gh is read once: both sums over the channels are taken while the tile lies in
 // registers.  A workgroup keeps its threads' share of the channels for its whole life, so dw is summed in
-// registers over the workgroup's tiles (each term rounded to fp32, their sum in fp64), then over its lanes, and
+// registers over the workgroup's tiles (the terms and their sum in fp64), then over its lanes, and
 // the workgroups' partial rows are summed in fp64 by a second launch.  Rows too long for that have dw summed by a
 // launch of its own (dw_rows_kernel).  Every order is fixed, so results are bitwise reproducible.
 //
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_cols_kernel(BwdArgs a)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd[e];
-                acc[j] += e >= pos.dup ? (double)(gy[e] * u) : 0.0;
+                acc[j] = e >= pos.dup ? __builtin_fma((double)gy[e], (double)u, acc[j]) : acc[j];
                 o[e] = rstd[e] * (gy[e] * w[j] - u * c[e]);
             }
             if constexpr (RES) {
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_rows_kernel(BwdArgs a)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const float u = h[e] * rstd;
-                if constexpr (DW) acc[k][e] += live && e >= pos[k].dup ? (double)(gy[e] * u) : 0.0;
+                if constexpr (DW) acc[k][e] = live && e >= pos[k].dup ? __builtin_fma((double)gy[e], (double)u, acc[k][e]) : acc[k][e];
                 o[e] = rstd * (gy[e] * wk[e] - u * c);
             }
             if constexpr (RES) {
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kDwThreads) void dw_rows_kernel(BwdArgs a, int64_t 
                 unpack(ph[u], h);
                 unpack(pg[u], gy);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[e] += (double)(gy[e] * (h[e] * rstd[u]));
+                for (int e = 0; e < VEC; ++e) acc[e] = __builtin_fma((double)gy[e], (double)(h[e] * rstd[u]), acc[e]);
             }
     }
 #pragma unroll
@@ -436,7 +436,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void bwd_loop_kernel(BwdArgs a)
             store_elem((T *)a.gx + base, (int64_t)c * a.M, o);
             if (a.rstd) continue;  // uniform
             // P <= 64 lanes of one wave walk together
-            const double d = join_run(pos.dup ? 0.0 : (double)(gy * u), a.lg, AddOp());
+            const double d = join_run(pos.dup ? 0.0 : (double)gy * (double)u, a.lg, AddOp());
             if (lane == 0) mine[c] = tile == blockIdx.x ? d : mine[c] + d;
         }
     }
