@@ -7,9 +7,9 @@
 // Everything between the loads and the one rounding of each output is fp32: the sum h before it is
 // rounded for storage, the mean of squares, y and the scales.  Memory traffic bounds every size beyond
 // the smallest (4 to 7 flops an element), so each element is read once and held in registers from the
-// sum to the write.  With a residual, 2x256x721x1440 bf16 takes 745-842 us from card to card (5.1-5.7 TB/s; a copy in
+// sum to the write.  With a residual, 2x256x721x1440 bf16 takes 745-847 us from card to card (5.1-5.7 TB/s; a copy in
 // the same 512-byte runs 790-870, a linear one 724-760), 4x32x181x360 fp32 19.4 us, rows of 512 bf16 176 us for
-// 259200 (6.0 TB/s); 8 bits, 1x80x721x1440 bf16 109-121 us, 259200x512 fp16 without a residual 75 us (5.3 TB/s).
+// 259200 (6.0 TB/s); 8 bits, 1x80x721x1440 bf16 117-121 us, 259200x512 fp16 without a residual 73 us (5.4 TB/s).
 #include "kernels.hpp"
 #include "norm.hpp"
 #include "norm_device.hpp"

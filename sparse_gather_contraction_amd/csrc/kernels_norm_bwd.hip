@@ -12,8 +12,8 @@
 // the workgroups' partial rows are summed in fp64 by a second launch.  Rows too long for that have dw summed by a
 // launch of its own (dw_rows_kernel).  Every order is fixed, so results are bitwise reproducible.
 //
-// Memory bounds it: 2x256x721x1440 bf16 with gh 781-856 us from card to card (5.0-5.4 TB/s; a copy in the same
-// 256-byte runs takes 815-930), 259200x512 bf16 193 us (5.5 TB/s), 4x32x181x360 fp32 21.7 us and 3.9 of the second launch.
+// Memory bounds it: 2x256x721x1440 bf16 with gh 781-862 us from card to card (4.9-5.4 TB/s; a copy in the same
+// 256-byte runs takes 815-930), 259200x512 bf16 195 us (5.4 TB/s), 4x32x181x360 fp32 21.5 us and 3.8 of the second launch.
 #include "kernels.hpp"
 #include "norm.hpp"
 #include "norm_device.hpp"
