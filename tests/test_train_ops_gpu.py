@@ -701,3 +701,44 @@ def test_written_tensors_count_as_changed_in_place():
         t = torch.full((64,), 3.0, device=DEV)
     sgc.disco_clip_grads([t], 1e-3)
     assert float(t[0]) < 1
+
+
+BWD_PATHS = [((259, 512), -1), ((40, 9000), -1), ((40, 20000), -1), ((20, 40000), -1), ((2, 80, 20, 33), 1), ((900, 24, 3), 1), ((1, 1040, 96, 97), 1)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", BWD_PATHS, ids=ids)
+def test_bwd_workspace_at_fp32_alignment(case, dtype):
+    # four bytes past an allocation's start is alignment enough, and nothing outside of the workspace is written
+    shape, axis = case
+    print(f"[workspace] {shape} axis {axis} {dtype}", flush=True)
+    h, gy = randn(shape, T[dtype], 221), randn(shape, T[dtype], 222)
+    w = randn((shape[axis],), torch.float32, 223)
+    want = sgc.disco_rms_norm_bwd(h, w, gy, axis=axis, eps=EPS)
+    need = sgc.disco_rms_norm_bwd_workspace(h, axis=axis)
+    ws = torch.full((need + 68,), 0x5a, dtype=torch.uint8, device=DEV)
+    got = sgc.disco_rms_norm_bwd(h, w, gy, axis=axis, eps=EPS, workspace=ws[4:4 + need])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((ws[:4] == 0x5a).all()) and bool((ws[4 + need:] == 0x5a).all())
+    with pytest.raises(sgc.DiscoError):
+        sgc.disco_rms_norm_bwd(h, w, gy, axis=axis, eps=EPS, workspace=ws[:need - 1])
+
+
+@pytest.mark.parametrize("case", BWD_PATHS, ids=ids)
+def test_graph_replays_of_the_backward(case):
+    shape, axis = case
+    print(f"[graph] {shape} axis {axis}", flush=True)
+    h, gy = randn(shape, torch.bfloat16, 231), randn(shape, torch.bfloat16, 232)
+    w = randn((shape[axis],), torch.float32, 233)
+    sgc.disco_rms_norm_bwd(h, w, gy, gh=gy, axis=axis)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = sgc.disco_rms_norm_bwd(h, w, gy, gh=gy, axis=axis)
+    for k in range(4):
+        h.copy_(randn(shape, torch.bfloat16, 240 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = sgc.disco_rms_norm_bwd(h, w, gy, gh=gy, axis=axis)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), f"replay {k}"
