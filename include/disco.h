@@ -64,8 +64,16 @@ typedef enum disco_dtype {
     DISCO_BF16 = 1,
     DISCO_F16 = 2,
     DISCO_F8_E4M3 = 3,        /* 8-bit forms (OCP): disco_rms_norm_f8 and disco_dequantize only */
-    DISCO_F8_E5M2 = 4
+    DISCO_F8_E5M2 = 4,
+    DISCO_I8 = 5              /* the 8-bit form of the channel products: disco_quantize_i8 and what reads it */
 } disco_dtype;
+
+/* Activation functions of the channel products. */
+typedef enum disco_act {
+    DISCO_ACT_NONE = 0,
+    DISCO_ACT_GELU = 1,       /* x Phi(x), Phi the normal distribution function (erf form) */
+    DISCO_ACT_SILU = 2        /* x / (1 + e^-x) */
+} disco_act;
 
 /* Host-side CSR filter ("psi").  Rows r = k*Ho + ho, K*Ho rows in all.
  * Column of an entry = input pixel (col_hi[e], col_wi[e]): the input latitude
@@ -270,6 +278,62 @@ disco_status disco_grad_norm(int64_t n, const disco_tensor *grads, disco_tensor 
  * one makes finite elements 0 and infinite ones NaN, whatever max_norm is.  The factor stays on the device. */
 disco_status disco_clip_grads(int64_t n, const disco_tensor *grads, float max_norm, float eps, disco_tensor *outs,
                               disco_tensor *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- channel products in 8-bit integers, and 8-bit activation checkpoints ---------------------------------
+ *
+ * The pointwise product of a residual block, y = x W^T + bias over the channels of each point, with its operands in 8 bits,
+ * for inference and for training (the forward's operand is the checkpoint that the backward reads).  No psi; the current
+ * device; tensors, alignment, overlaps, rounding, reproducibility and graph capture as for the training-step operators
+ * above.  `axis` is the channel axis of the dense tensor: 1 for fields (B, C, H, W), the last one for rows (points, C).
+ *
+ * The 8-bit form of a tensor over its channels (C of them):
+ *   scale[p] = max(max over c of |x[p,c]| / 127, 2^-126),   q[p,c] = x[p,c] / scale[p] to whole numbers (ties to even)
+ * q: DISCO_I8, the tensor's shape with the channel axis moved last and padded to Cp, the next multiple of 16, with zeros;
+ * 16-byte aligned.  scale: F32, the tensor's shape without the channel axis.  A point that holds a NaN or an infinity has
+ * scale NaN and q 0.  A weight (Co, C) takes the same form over its last axis: w (Co, Cp), wscale (Co).
+ * At most 2^31 - 4096 points (and output channels), at most 131056 padded channels in a product (so that its sums, also
+ * of q = -128, stay below 2^31). */
+
+/* The form of act(x).  x: F32, BF16 or F16, 1 to 5 dimensions.  kept, kept_scale: both NULL, or the form of x itself, the
+ * checkpoint that disco_linear_i8_bwd_input takes the function's slope from (only with an activation function: without
+ * one it is q).  act is evaluated in fp32. */
+disco_status disco_quantize_i8(const disco_tensor *x, disco_act act, int axis, disco_tensor *q, disco_tensor *scale,
+                               disco_tensor *kept, disco_tensor *kept_scale, void *stream);
+
+/* out = q scale: the reader.  out: F32, BF16 or F16, dense, its channel axis `axis` of C entries with C padded to 16
+ * giving q's last dimension. */
+disco_status disco_dequantize_i8(const disco_tensor *q, const disco_tensor *scale, int axis, disco_tensor *out,
+                                 void *stream);
+
+/* y[p,o] = scale[p] wscale[o] sum_c q[p,c] w[o,c] + bias[o].  q (points..., Cp), scale (points...), w (Co, Cp), wscale
+ * (Co), bias (Co) F32 or NULL; y: F32, BF16 or F16, the points' shape with the Co channels at `axis`.  The sum is exact;
+ * it is converted to fp32, multiplied by scale[p], then by wscale[o], the bias added, and y rounded once.  All Cp places
+ * are multiplied, so what lies behind C has to be 0 in q or in w. */
+disco_status disco_linear_i8(const disco_tensor *q, const disco_tensor *scale, const disco_tensor *w,
+                             const disco_tensor *wscale, const disco_tensor *bias, int axis, disco_tensor *y,
+                             void *stream);
+
+/* Gradient of the product's input, and with `act` of what the activation function before the product was taken of:
+ *   gx[p,c] = act'(kept[p,c] kept_scale[p]) sum_o gy[p,o] wscale[o] w[o,c]
+ * gy, gx: BF16 or F16, both alike, dense, channels at `axis` (Co in gy, C in gx); w (Co, Cp), wscale (Co) as above, C
+ * padded to 16 giving Cp; kept (points..., Cp) and kept_scale (points...) with an activation function, NULL without one.
+ * wscale w is rounded to the data type (RNE), the sum is fp32. */
+disco_status disco_linear_i8_bwd_input(const disco_tensor *gy, const disco_tensor *w, const disco_tensor *wscale,
+                                       disco_act act, const disco_tensor *kept, const disco_tensor *kept_scale,
+                                       int axis, disco_tensor *gx, void *stream);
+
+/* Gradients of the product's weight and bias:
+ *   dw[o,c] = sum_p gy[p,o] scale[p] q[p,c],   db[o] = sum_p gy[p,o]
+ * gy: BF16 or F16, dense, its Co channels at `axis`; q (points..., Cp), scale (points...): the 8-bit operand that the
+ * forward took; dw (Co, C) and db (Co) or NULL, of gy's type.  scale q is rounded to the data type (RNE) as the reader
+ * writes it; sums are fp32 in runs of points and fp64 over the runs, in a fixed order.  With no points both are zeros.
+ * `workspace` is caller-owned device memory (16-byte aligned) of at least the size that
+ * disco_linear_i8_bwd_weight_workspace reports for these tensors (their data is not read; db: whether there is one); its
+ * contents on entry are ignored; may be NULL where the size is 0.  Calls sharing one workspace must not overlap. */
+disco_status disco_linear_i8_bwd_weight_workspace(const disco_tensor *gy, int axis, int64_t C, int db, size_t *bytes);
+disco_status disco_linear_i8_bwd_weight(const disco_tensor *gy, const disco_tensor *q, const disco_tensor *scale,
+                                        int axis, disco_tensor *dw, disco_tensor *db, void *workspace,
+                                        size_t workspace_bytes, void *stream);
 
 /* Message of the last non-OK status returned on the calling thread ("" if none). */
 const char *disco_last_error(void);

@@ -10,7 +10,7 @@ The names mirror the C ABI in ``include/disco.h``:
     gx  = disco_bwd(psi, gout)               # (B,C,K,Ho,Wo) -> (B,C,Hi,Wi)
     y   = disco_fused_conv(psi, x, W)        # (B,C,Hi,Wi), (Co,C,K) -> (B,Co,Ho,Wo)
 
-The operators around the convolution in a training step (disco_rms_norm and below) are marshalled by a
+The operators around the convolution (disco_rms_norm and below) are marshalled by a
 compiled module, ``_disco_bind.so`` (csrc/bind.cpp), in the same way.
 
 There is no fallback: if a library is not built, loading raises.
@@ -41,11 +41,14 @@ DISCO_BF16 = 1
 DISCO_F16 = 2
 DISCO_F8_E4M3 = 3
 DISCO_F8_E5M2 = 4
+DISCO_I8 = 5
+ACTS = {None: 0, "gelu": 1, "silu": 2}  # disco_act: activation functions of the channel products
 EXPORTED = ("disco_psi_create", "disco_psi_destroy", "disco_fwd", "disco_bwd", "disco_fused_conv",
             "disco_fused_conv_save", "disco_einsum", "disco_fused_conv_bwd_workspace", "disco_fused_conv_bwd",
             "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc", "disco_rms_norm", "disco_rms_norm_f8",
             "disco_dequantize", "disco_rms_norm_bwd_workspace", "disco_rms_norm_bwd", "disco_grad_norm_workspace",
-            "disco_grad_norm", "disco_clip_grads", "disco_last_error")
+            "disco_grad_norm", "disco_clip_grads", "disco_quantize_i8", "disco_dequantize_i8", "disco_linear_i8",
+            "disco_linear_i8_bwd_input", "disco_linear_i8_bwd_weight_workspace", "disco_linear_i8_bwd_weight", "disco_last_error")
 
 
 class DiscoError(RuntimeError):
@@ -99,12 +102,20 @@ def load_library():
         lib.disco_grad_norm_workspace.argtypes = [I64, P, ctypes.POINTER(SZ)]
         lib.disco_grad_norm.argtypes = [I64, P, T, P, SZ, P]
         lib.disco_clip_grads.argtypes = [I64, P, F, F, P, T, P, SZ, P]
+        lib.disco_quantize_i8.argtypes = [T, ctypes.c_int, ctypes.c_int, T, T, T, T, P]
+        lib.disco_dequantize_i8.argtypes = [T, T, ctypes.c_int, T, P]
+        lib.disco_linear_i8.argtypes = [T, T, T, T, T, ctypes.c_int, T, P]
+        lib.disco_linear_i8_bwd_input.argtypes = [T, T, T, ctypes.c_int, T, T, ctypes.c_int, T, P]
+        lib.disco_linear_i8_bwd_weight_workspace.argtypes = [T, ctypes.c_int, I64, ctypes.c_int, ctypes.POINTER(SZ)]
+        lib.disco_linear_i8_bwd_weight.argtypes = [T, T, T, ctypes.c_int, T, T, P, SZ, P]
         lib.disco_last_error.restype = ctypes.c_char_p
         for f in ("disco_psi_create", "disco_psi_destroy", "disco_fwd", "disco_bwd", "disco_fused_conv",
                   "disco_fused_conv_save", "disco_einsum", "disco_fused_conv_bwd_workspace", "disco_fused_conv_bwd",
                   "disco_fused_conv_bwd_saved", "disco_fused_conv_bwd_noalloc", "disco_rms_norm", "disco_rms_norm_f8",
                   "disco_dequantize", "disco_rms_norm_bwd_workspace", "disco_rms_norm_bwd",
-                  "disco_grad_norm_workspace", "disco_grad_norm", "disco_clip_grads"):
+                  "disco_grad_norm_workspace", "disco_grad_norm", "disco_clip_grads", "disco_quantize_i8", "disco_dequantize_i8",
+                  "disco_linear_i8", "disco_linear_i8_bwd_input", "disco_linear_i8_bwd_weight_workspace",
+                  "disco_linear_i8_bwd_weight"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -416,3 +427,67 @@ def disco_clip_grads(grads, max_norm, out=None, eps=1e-6, device=None):
     In place, or into the tensors of the list `out`.  The factor never leaves the device."""
     grads = grads if type(grads) is list else list(grads)
     return (_bind or _binding()).clip_grads(grads, max_norm, eps, out, _result_on(grads, device))
+
+
+# ---- channel products in 8-bit integers, and 8-bit activation checkpoints
+
+
+def _act_code(act) -> int:
+    try:
+        return ACTS[act]
+    except (KeyError, TypeError):
+        raise DiscoError(1, "act must be None, 'gelu' or 'silu'") from None
+
+
+def _channels(channels) -> int:
+    if channels is None:
+        return -1
+    if channels < 0:
+        raise DiscoError(2, "the number of channels is out of range")
+    return channels
+
+
+def disco_quantize_i8(x, act=None, keep=False, axis=1, q=None, scale=None, kept=None, kept_scale=None):
+    """The 8-bit form of act(x) over its channel axis: (q, scale), or with `keep` (q, scale, kept, kept_scale).
+
+    q (int8) holds a point's channels together, in x's shape with `axis` moved last and padded with zeros to a multiple of
+    16; scale (fp32) has x's shape without `axis`.  act is None, "gelu" or "silu".  kept and kept_scale are the form of x
+    itself, the checkpoint that disco_linear_i8_bwd_input takes act's slope from.  A weight (Co, C) takes axis=1."""
+    return (_bind or _binding()).quantize_i8(x, _act_code(act), keep or kept is not None or kept_scale is not None, axis, q, scale,
+                                             kept, kept_scale)
+
+
+def disco_dequantize_i8(q, scale, channels=None, dtype=None, axis=1, out=None):
+    """out = q * scale in `dtype` (default bf16, or the given out's), `channels` of them (default: all of q's) at `axis`."""
+    code = DISCO_BF16 if dtype is None else _data_code(dtype, out)
+    return (_bind or _binding()).dequantize_i8(q, scale, _channels(channels), code, axis, out)
+
+
+def disco_linear_i8(q, scale, w, wscale, bias=None, dtype=None, axis=1, out=None):
+    """y = (q scale) (w wscale)^T + bias over the channels of each point, from the 8-bit forms of both.
+
+    q (points..., Cp), scale (points...): disco_quantize_i8 of the input; w (Co, Cp), wscale (Co): of the weight; bias (Co)
+    fp32.  y has the Co channels at `axis`, in `dtype` (default bf16, or the given out's)."""
+    code = DISCO_BF16 if dtype is None else _data_code(dtype, out)
+    return (_bind or _binding()).linear_i8(q, scale, w, wscale, bias, code, axis, out)
+
+
+def disco_linear_i8_bwd_input(gy, w, wscale, channels=None, act=None, kept=None, kept_scale=None, axis=1, gx=None):
+    """The gradient of disco_linear_i8's input (before it was put into 8 bits): gy w, channels at `axis` of both.
+
+    With act, kept and kept_scale the gradient of what act was taken of before the product: times act'(kept kept_scale).
+    `channels` is the input's number of channels (default: all of w's)."""
+    return (_bind or _binding()).linear_i8_bwd_input(gy, w, wscale, _channels(channels), _act_code(act), kept, kept_scale, axis, gx)
+
+
+def disco_linear_i8_bwd_weight_workspace(gy, channels, bias=False, axis=1) -> int:
+    """Workspace bytes disco_linear_i8_bwd_weight needs for this gy."""
+    return _binding().linear_i8_bwd_weight_workspace(gy, channels, bias, axis)
+
+
+def disco_linear_i8_bwd_weight(gy, q, scale, channels=None, bias=False, axis=1, dw=None, db=None, workspace=None):
+    """dw, or (dw, db) with `bias`: the gradients of disco_linear_i8's weight (Co, channels) and bias (Co).
+
+    q, scale: the 8-bit input that the forward took; gy has its Co channels at `axis`.  The workspace (a uint8 device
+    tensor) is allocated here when not given."""
+    return (_bind or _binding()).linear_i8_bwd_weight(gy, q, scale, _channels(channels), bias or db is not None, axis, dw, db, workspace)

@@ -15,15 +15,16 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdisco.so")
-BIND = os.path.join(PKG, "_disco_bind.so")   # the marshalling of the training-step operators, on top of LIB
+BIND = os.path.join(PKG, "_disco_bind.so")   # the marshalling of the operators without a psi, on top of LIB
 PROBE_LIB = os.path.join(PKG, "libdisco_probes.so")  # microbenchmarks of the device (measurement only)
 
 SOURCES = ["plan.cpp", "plan_fused.cpp", "plan_tile.cpp", "kernels_tile.hip", "disco_api.hip", "kernels_gather.hip", "kernels_staged.hip", "kernels_fused.hip",
            "kernels_fused_mfma.hip", "kernels_gemm.hip", "norm_api.hip", "kernels_norm.hip", "kernels_norm_bwd.hip",
-           "kernels_grad.hip"]
+           "kernels_grad.hip", "linear_api.hip", "kernels_form.hip", "kernels_linear.hip", "kernels_linear_bwd.hip"]
 # Built with unaligned memory access: their vectors lie at any element (odd sizes, views into a flat buffer),
 # and they read no LDS at less than its type's alignment.
-UNALIGNED = {"kernels_norm.hip", "kernels_norm_bwd.hip", "kernels_grad.hip"}
+UNALIGNED = {"kernels_norm.hip", "kernels_norm_bwd.hip", "kernels_grad.hip", "kernels_form.hip", "kernels_linear.hip",
+             "kernels_linear_bwd.hip"}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -81,7 +82,7 @@ def _link_bind(obj: str) -> None:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=4) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
         bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
         bind_obj = bind.result()

@@ -1,4 +1,4 @@
-// bind.cpp — the binding of the training-step operators: torch tensors to disco_tensor views, outputs and
+// bind.cpp — the binding of the operators without a psi: torch tensors to disco_tensor views, outputs and
 // workspaces that the caller did not give, torch's current stream, a status to an exception.
 //
 // A call on little data costs the host's time alone, and a call on many gradients the host's time per tensor;
@@ -32,6 +32,7 @@ disco_dtype code_of(at::ScalarType t)
     case at::kHalf: return DISCO_F16;
     case at::kFloat8_e4m3fn: return DISCO_F8_E4M3;
     case at::kFloat8_e5m2: return DISCO_F8_E5M2;
+    case at::kChar: return DISCO_I8;
     default: return (disco_dtype)99;  // refused by the library
     }
 }
@@ -348,6 +349,158 @@ PyObject *clip_grads(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded(n, 5, [&] { return grads_call(a[0], a[4], true, (float)real(a[1]), (float)real(a[2]), a[3]); });
 }
 
+// ---- channel products in 8-bit integers
+
+at::ScalarType type_of(long long code) { return code == DISCO_F32 ? at::kFloat : code == DISCO_F16 ? at::kHalf : at::kBFloat16; }
+
+// The points of a dense tensor: its shape without the channel axis.  An axis that is out of range takes nothing away (the
+// library refuses it).
+std::vector<int64_t> points_of(const at::Tensor &x, int axis)
+{
+    auto shape = x.sizes().vec();
+    const int64_t i = axis < 0 ? axis + x.dim() : axis;
+    if (i >= 0 && i < x.dim()) shape.erase(shape.begin() + i);
+    return shape;
+}
+
+// The form of a dense tensor, made where it is not given.
+void make_form(const at::Tensor &x, int axis, Arg *q, Arg *scale)
+{
+    const int64_t i = axis < 0 ? axis + x.dim() : axis;
+    const int64_t D = i >= 0 && i < x.dim() ? x.size(i) : 1;
+    auto shape = points_of(x, axis);
+    if (!scale->given) scale->set(at::empty(shape, x.options().dtype(at::kFloat).requires_grad(false)));
+    if (q->given) return;
+    shape.push_back((D + 15) / 16 * 16);
+    q->set(at::empty(shape, x.options().dtype(at::kChar).requires_grad(false)));
+}
+
+// The dense tensor of a form's points with `D` channels at `axis`.
+at::Tensor dense_of(const at::Tensor &q, long long D, int axis, at::ScalarType type)
+{
+    auto shape = q.sizes().vec();
+    if (!shape.empty()) shape.pop_back();
+    const int64_t i = axis < 0 ? axis + (int64_t)shape.size() + 1 : axis;
+    shape.insert(shape.begin() + (i >= 0 && i <= (int64_t)shape.size() ? i : (int64_t)shape.size()), D < 0 ? 0 : D);
+    return at::empty(shape, q.options().dtype(type));
+}
+
+// quantize_i8(x, act, keep, axis, q, scale, kept, kept_scale)
+PyObject *quantize_i8(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 8, [&]() -> PyObject * {
+        Required x(a[0]);
+        Arg q(a[4]), scale(a[5]), kept(a[6]), ks(a[7]);
+        const long long act = whole(a[1]);
+        const int keep = PyObject_IsTrue(a[2]), axis = axis_of(a[3]);
+        if (keep < 0) throw Raised();
+        make_form(x.t, axis, &q, &scale);
+        if (keep) make_form(x.t, axis, &kept, &ks);
+        void *s = stream_of(x.t);
+        call([&] { return disco_quantize_i8(&x.d, (disco_act)act, axis, &q.d, &scale.d, kept.ptr(), ks.ptr(), s); });
+        if (!kept.given) return pair(q.out(), scale.out());
+        PyObject *o[4] = {q.out(), scale.out(), kept.out(), ks.out()};
+        PyObject *t = o[0] && o[1] && o[2] && o[3] ? PyTuple_Pack(4, o[0], o[1], o[2], o[3]) : nullptr;
+        for (PyObject *v : o) Py_XDECREF(v);
+        return t;
+    });
+}
+
+// dequantize_i8(q, scale, channels or -1, code of the output's type, axis, out)
+PyObject *dequantize_i8(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 6, [&] {
+        Required q(a[0]), scale(a[1]);
+        Arg out(a[5]);
+        const int axis = axis_of(a[4]);
+        if (!out.given) {
+            const long long D = whole(a[2]);
+            out.set(dense_of(q.t, D < 0 && q.t.dim() ? q.t.size(-1) : D, axis, type_of(whole(a[3]))));
+        }
+        void *s = stream_of(q.t);
+        call([&] { return disco_dequantize_i8(&q.d, &scale.d, axis, &out.d, s); });
+        return out.out();
+    });
+}
+
+// linear_i8(q, scale, w, wscale, bias, code of the output's type, axis, out)
+PyObject *linear_i8(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        Required q(a[0]), scale(a[1]), w(a[2]), wscale(a[3]);
+        Arg bias(a[4]), y(a[7]);
+        const int axis = axis_of(a[6]);
+        if (!y.given) y.set(dense_of(q.t, w.t.dim() ? w.t.size(0) : 0, axis, type_of(whole(a[5]))));
+        void *s = stream_of(q.t);
+        call([&] { return disco_linear_i8(&q.d, &scale.d, &w.d, &wscale.d, bias.ptr(), axis, &y.d, s); });
+        return y.out();
+    });
+}
+
+// linear_i8_bwd_input(gy, w, wscale, channels or -1, act, kept, kept_scale, axis, gx)
+PyObject *linear_i8_bwd_input(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 9, [&] {
+        Required gy(a[0]), w(a[1]), wscale(a[2]);
+        Arg kept(a[5]), ks(a[6]), gx(a[8]);
+        const long long act = whole(a[4]);
+        const int axis = axis_of(a[7]);
+        if (!gx.given) {
+            const long long D = whole(a[3]);
+            auto shape = gy.t.sizes().vec();
+            const int64_t i = axis < 0 ? axis + gy.t.dim() : axis;
+            if (i >= 0 && i < gy.t.dim()) shape[i] = D >= 0 ? D : w.t.dim() ? w.t.size(-1) : 0;
+            gx.set(at::empty(shape, gy.t.options()));
+        }
+        void *s = stream_of(gy.t);
+        call([&] { return disco_linear_i8_bwd_input(&gy.d, &w.d, &wscale.d, (disco_act)act, kept.ptr(), ks.ptr(), axis, &gx.d, s); });
+        return gx.out();
+    });
+}
+
+// linear_i8_bwd_weight(gy, q, scale, channels or -1, bias, axis, dw, db, workspace)
+PyObject *linear_i8_bwd_weight(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 9, [&]() -> PyObject * {
+        Required gy(a[0]), q(a[1]), scale(a[2]);
+        Arg dw(a[6]), db(a[7]), ws(a[8]);
+        const int bias = PyObject_IsTrue(a[4]), axis = axis_of(a[5]);
+        if (bias < 0) throw Raised();
+        const int64_t i = axis < 0 ? axis + gy.t.dim() : axis;
+        const int64_t Co = i >= 0 && i < gy.t.dim() ? gy.t.size(i) : 1;
+        if (!dw.given) {
+            const long long D = whole(a[3]);
+            dw.set(at::empty({Co, D >= 0 ? D : q.t.dim() ? q.t.size(-1) : 0}, gy.t.options()));
+        }
+        if (bias && !db.given) db.set(at::empty({Co}, gy.t.options()));
+        if (!ws.given) {
+            size_t need = 0;
+            check(disco_linear_i8_bwd_weight_workspace(&gy.d, axis, dw.t.dim() ? dw.t.size(-1) : 0, db.given, &need));
+            if (need) ws.set(bytes_on(gy.t, need));
+        }
+        void *s = stream_of(gy.t);
+        call([&] {
+            return disco_linear_i8_bwd_weight(&gy.d, &q.d, &scale.d, axis, &dw.d, db.ptr(), ws.given ? ws.d.data : nullptr,
+                                              ws.given ? ws.t.nbytes() : 0, s);
+        });
+        return db.given ? pair(dw.out(), db.out()) : dw.out();
+    });
+}
+
+// linear_i8_bwd_weight_workspace(gy, channels, bias, axis)
+PyObject *linear_i8_bwd_weight_workspace(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded(n, 4, [&]() -> PyObject * {
+        Required gy(a[0]);
+        const long long C = whole(a[1]);
+        const int bias = PyObject_IsTrue(a[2]), axis = axis_of(a[3]);
+        if (bias < 0) throw Raised();
+        size_t need = 0;
+        check(disco_linear_i8_bwd_weight_workspace(&gy.d, axis, C, bias, &need));
+        return PyLong_FromSize_t(need);
+    });
+}
+
 // setup(DiscoError, device index -> current stream)
 PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -364,7 +517,8 @@ PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(setup), FAST(rms_norm), FAST(rms_norm_f8), FAST(dequantize), FAST(rms_norm_bwd),
-                           FAST(grad_norm), FAST(clip_grads), {nullptr, nullptr, 0, nullptr}};
+                           FAST(grad_norm), FAST(clip_grads), FAST(quantize_i8), FAST(dequantize_i8), FAST(linear_i8),
+                           FAST(linear_i8_bwd_input), FAST(linear_i8_bwd_weight), FAST(linear_i8_bwd_weight_workspace), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_disco_bind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,176 @@
+// linear_check.cpp — replays the index arithmetic of the 8-bit form and the channel products on the CPU.
+//
+//   linear_check          (built by the tests with g++ and the address and undefined-behaviour sanitizers)
+//
+// Walks the form's writer and reader as the kernels do, for many shapes and element sizes (every access inside its tensor,
+// every element and code met, the LDS indexes inside what a launch asks for, a tile's codes read where they were written),
+// and checks the division by a product, the products' LDS layouts, the map of workgroups to tiles and the splits of the
+// weight's gradient.  Prints the number of geometries checked.
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+
+#include "linear_plan.hpp"
+
+using namespace disco;
+
+static void fail(const char *what, int64_t a, int64_t b, int64_t c, int d)
+{
+    printf("FAILED: %s at %lld, %lld, %lld, %d\n", what, (long long)a, (long long)b, (long long)c, d);
+    exit(1);
+}
+
+#define REQUIRE(x) do { if (!(x)) fail(#x, N, D, M, esz); } while (0)
+
+static void check_form(int64_t N, int64_t D, int64_t M, int esz)
+{
+    const FormGeom g = form_geom(N, D, M, esz);
+    const int64_t Dp = padded_channels(D), P = N * M;
+    const int nv = (int)(Dp / kFormChannels), lanes = 1 << g.lg;
+    REQUIRE(Dp % 16 == 0 && Dp >= D && Dp < D + 16);
+    REQUIRE(g.threads >= 64 && g.threads <= kNormMaxThreads && g.threads % 64 == 0 && g.tiles >= 1);
+    REQUIRE(form_lds_bytes(g, Dp) <= 80 * 1024);
+    std::vector<int> codes((size_t)(P * nv), 0), held((size_t)(N * D * M), 0);
+    if (g.loop) {
+        const int groups = g.threads >> g.lg;
+        REQUIRE(form_lds_bytes(g, Dp) >= (size_t)2 * lanes * 4 && groups * lanes == g.threads && g.vec == 1);
+        for (int64_t tile = 0; tile < g.tiles; ++tile)
+            for (int t = 0; t < g.threads; ++t) {
+                const ColPos p = col_pos(tile, t & (lanes - 1), 1, g.lg, 1, N, M);
+                REQUIRE(p.n >= 0 && p.n < N && p.m >= 0 && p.m < M);
+                for (int64_t c = (int64_t)(t >> g.lg) * 8; c < Dp; c += (int64_t)groups * 8) {
+                    REQUIRE(c + 8 <= Dp);
+                    if (!p.dup) ++codes[(size_t)((p.n * M + p.m) * nv + c / 8)];
+                    for (int64_t j = c; j < c + 8 && j < D; ++j)
+                        if (!p.dup) ++held[(size_t)((p.n * D + j) * M + p.m)];
+                }
+            }
+    } else if (g.rows) {
+        REQUIRE(M == 1 && g.slots * lanes == g.threads && (int64_t)g.per * lanes >= nv);
+        for (int64_t tile = 0; tile < g.tiles; ++tile)
+            for (int t = 0; t < g.threads; ++t) {
+                const int64_t want = tile * g.slots + (t >> g.lg), row = want < N ? want : N - 1;
+                for (int k = 0; k < g.per; ++k) {
+                    const int64_t c = (int64_t)(k * lanes + (t & (lanes - 1))) * 8;
+                    if (c < Dp && want < N) ++codes[(size_t)(row * nv + c / 8)];
+                    for (int64_t j = c; j < c + 8 && j < D; ++j)
+                        if (want < N) ++held[(size_t)(row * D + j)];
+                }
+            }
+    } else {
+        const int PT = lanes * g.vec, half = nv / 2;
+        REQUIRE(g.slots == nv && g.threads >= nv * lanes && form_lds_bytes(g, Dp) == (size_t)PT * Dp + (size_t)PT * 8);
+        const FastDiv by = fast_div((uint32_t)half);
+        for (int64_t tile = 0; tile < g.tiles; ++tile) {
+            std::vector<int64_t> lds((size_t)PT * nv, -1);   // which code (point, eight) lies there
+            for (int t = 0; t < g.threads; ++t) {
+                const int lane = t & (lanes - 1), grp = t >> g.lg;
+                const ColPos p = col_pos(tile, lane, g.vec, g.lg, g.tiles_n, N, M);
+                REQUIRE(p.n >= 0 && p.n < N && p.m >= 0 && p.m + g.vec <= M && p.dup >= 0);
+                if (grp >= nv) continue;
+                int cg = grp + lane % nv;
+                if (cg >= nv) cg -= nv;
+                for (int e = 0; e < g.vec; ++e) {
+                    const int at = (lane * g.vec + e) * nv + cg;
+                    REQUIRE(at * 8 == form_lds(lane * g.vec + e, grp, nv, lane) && at < PT * nv && lds[at] < 0);
+                    lds[at] = (p.n * M + p.m + e) * nv + grp;
+                    for (int j = grp * 8; j < grp * 8 + 8 && j < D; ++j)
+                        if (e >= p.dup) ++held[(size_t)((p.n * D + j) * M + p.m + e)];
+                }
+            }
+            for (int i = 0; i < PT * half; ++i) {
+                const int pt = (int)by.div(i), h = i - pt * half, l = pt / g.vec;
+                const ColPos at = col_pos(tile, l, g.vec, g.lg, g.tiles_n, N, M);
+                const int64_t point = at.n * M + at.m + (pt - l * g.vec);
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t code = lds[(size_t)form_lds(pt, 2 * h + k, nv, l) / 8];
+                    REQUIRE(code == point * nv + 2 * h + k);
+                    if (pt - l * g.vec >= at.dup) ++codes[(size_t)code];
+                }
+            }
+        }
+    }
+    for (int v : codes) REQUIRE(v == 1);
+    for (int v : held) REQUIRE(v == 1);
+}
+
+template <int N>
+static void check_across()
+{
+    std::vector<int> used(kBR * N * 2 / 16, 0);
+    for (int r = 0; r < kBR; ++r)
+        for (int n = 0; n < N; n += 8) {
+            const int at = bwd_across<N>(r, n);
+            if (at % 16 || at < 0 || at + 16 > kBR * N * 2 || used[at / 16]++) fail("across", N, r, n, 0);
+            for (int e = 0; e < 8; e += 4)  // what a transposing read takes: four elements
+                if (bwd_across<N>(r, n + e) != at + 2 * e) fail("across within a piece", N, r, n, e);
+        }
+}
+
+int main()
+{
+    int n = 0;
+    for (int64_t d : {1, 2, 3, 5, 7, 11, 64, 181, 360, 1000, 16471, 65535, 65536, 65537, 1038240, 2076480, (1 << 30) - 1, 1 << 30, 2147479552}) {
+        const FastDiv f = fast_div((uint32_t)d);
+        for (int64_t q = 0; q <= kMaxPoints / d; q += 1 + kMaxPoints / d / 5000)
+            for (int64_t k : {(int64_t)-1, (int64_t)0, (int64_t)1, d / 2, d - 1}) {
+                const int64_t v = q * d + k;
+                if (v >= 0 && v < ((int64_t)1 << 31) && f.div((uint32_t)v) != v / d) fail("division", v, d, 0, 0);
+            }
+        ++n;
+    }
+    for (int esz : {2, 4}) {
+        for (int64_t N : {1, 2, 5, 17})
+            for (int64_t D : {1, 8, 16, 17, 33, 80, 130, 256, 511, 600, 1030})
+                for (int64_t M : {1, 2, 5, 35, 63, 64, 65, 117, 260, 1031}) {
+                    check_form(N, D, M, esz);
+                    ++n;
+                }
+        for (int64_t D : {2047, 2048, 2049, 4097, 8192, 16385, 32768, 32769, 40000}) {
+            check_form(3, D, 1, esz);
+            check_form(1, D, 70, esz);
+            check_form(2, D, 5, esz);
+            n += 3;
+        }
+    }
+    check_form(700, 256, 1, 2);
+    check_form(1, 64, 66000, 2);  // tiles of the whole run
+    check_across<128>();
+    check_across<256>();
+    for (int rows : {128, 256}) {
+        std::vector<int> used(rows * 8, 0);
+        for (int r = 0; r < rows; ++r)
+            for (int p = 0; p < 8; ++p) {
+                const int at = bwd_along(r, p);
+                if (at % 16 || at < 0 || at + 16 > rows * kBR * 2 || used[at / 16]++) fail("along", rows, r, p, 0);
+            }
+        for (int s = 0; s < rows * 4; ++s)  // slot s is written by a direct load, read by row and piece
+            if (lin_at(s >> 2, lin_piece(s)) != 16 * s) fail("slot", rows, s, 0, 0);
+    }
+    for (int64_t total : {1, 7, 8, 9, 255, 256, 1000, 8104}) {
+        std::vector<int> met((size_t)total, 0);
+        for (int64_t i = 0; i < total; ++i) {
+            for (int32_t fast : {1, 3, 8}) {
+                int32_t a, b;
+                lin_tile(i, total, fast, &a, &b);
+                if (a < 0 || a >= fast || b < 0) fail("tile", total, i, fast, 0);
+                if (fast == 3 && (int64_t)b * 3 + a < total) ++met[(size_t)b * 3 + a];
+            }
+        }
+        for (int v : met)
+            if (v != 1) fail("tile met", total, v, 0, 0);
+    }
+    for (int64_t P : {(int64_t)1, (int64_t)63, (int64_t)64, (int64_t)65, (int64_t)1000, (int64_t)16400, (int64_t)70000, (int64_t)259200, (int64_t)2076480, kMaxPoints})
+        for (int64_t C : {1, 128, 129, 256, 512, 2048, 8192})
+            for (int64_t Co : {1, 73, 129, 256, 2048, 8192}) {
+                const WeightPlan p = weight_plan(P, C, Co);
+                const int64_t all = ceil_div64(P, kBR);
+                // every split has a step, and all steps have a split; a split's first point fits 32 bits
+                if (p.splits < 1 || p.steps < 1 || (int64_t)(p.splits - 1) * p.steps >= all || (int64_t)p.splits * p.steps < all ||
+                    (int64_t)p.splits * p.steps * kBR > ((int64_t)1 << 32)) fail("splits", P, C, Co, p.splits);
+                if (weight_bytes(p, C, Co, true) != (p.splits == 1 ? 0 : (size_t)p.splits * (Co * C + Co) * 4)) fail("bytes", P, C, Co, 0);
+                ++n;
+            }
+    printf("%d geometries checked\n", n);
+    return 0;
+}
