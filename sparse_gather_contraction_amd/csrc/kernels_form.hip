@@ -5,6 +5,8 @@
 //
 // Everything between the load and q is fp32, the quotient by the scale as it is stored, so that q scale is the nearest
 // such value to v.  A point that holds a NaN or an infinity has scale NaN and q 0: what is computed from it is NaN.
+#include <type_traits>
+
 #include "act_device.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
@@ -35,17 +37,21 @@ struct I8Scale {
 __device__ __forceinline__ I8Scale i8_scale(float amax)
 {
     if (!(amax < __builtin_inff())) return {__builtin_nanf(""), 0.0f, 0.0f};
-    const float s = __builtin_fmaxf(amax / 127.0f, 0x1p-126f);
-    return {s, __builtin_amdgcn_rcpf(s), s};
+    const float s = __builtin_fmaxf(amax / 127.0f, 0x1p-126f), r = __builtin_amdgcn_rcpf(s);
+    return {s, __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r), s};   // the reciprocal, rounded correctly but for rare ties
 }
 
 // Eight values to whole numbers in a byte each.  Added to 1.5 2^23 a quotient is rounded to a whole number (ties to even)
 // whose two's complement is the sum's low bits; |v / scale| <= 127 (1 + 2^-22), so none leaves a byte.
+// EXACT: the fp32 quotient.  Else (values of an activation function, which are off by more themselves) the product with the
+// rounded reciprocal, rounded once with that sum: within 127 2^-24 of the quotient.
+template <bool EXACT>
 __device__ __forceinline__ u32x2 i8_codes(const float (&v)[E], const I8Scale &s)
 {
     uint32_t b[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) b[i] = __float_as_uint(f8_quot(v[i], s.inv, s.back) + 12582912.0f);
+    for (int i = 0; i < E; ++i)
+        b[i] = __float_as_uint(EXACT ? f8_quot(v[i], s.inv, s.back) + 12582912.0f : __builtin_fmaf(v[i], s.inv, 12582912.0f));
     u32x2 r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -122,23 +128,23 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_rows_kernel(FormArgs
         }
         m = MaxOp()(m, amax_of(v[k]));
     }
-    auto write = [&](float amax, int8_t *q, float *scale) {
+    auto write = [&](auto exact, float amax, int8_t *q, float *scale) {
         const I8Scale s = i8_scale(amax);
         q += row * a.Dp;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             const int c = (k * lanes + tt) * E;
-            const u32x2 w = i8_codes(v[k], s);
+            const u32x2 w = i8_codes<decltype(exact)::value>(v[k], s);
             if (c < a.Dp) *(u32x2 *)(q + c) = w;
         }
         if (tt == 0) scale[row] = s.scale;
     };
-    write(row_max(m, a.lg, slots[0]), a.q, a.scale);
+    write(std::bool_constant<ACT == DISCO_ACT_NONE>(), row_max(m, a.lg, slots[0]), a.q, a.scale);
     if constexpr (ACT != DISCO_ACT_NONE)
         if (a.kq) {
 #pragma unroll
             for (int k = 0; k < KPT; ++k) unpack(px[k], v[k]);
-            write(row_max(mk, a.lg, slots[1]), a.kq, a.kscale);
+            write(std::true_type(), row_max(mk, a.lg, slots[1]), a.kq, a.kscale);
         }
 }
 
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_rows_kernel(FormArgs
 
 // A workgroup: 2^lg lanes along the points, nv threads along the channels.  LDS: [P][Dp] codes, [2][P] maxima.
 template <typename T, int ACT, int VEC>
-__global__ __launch_bounds__(kNormMaxThreads) void quantize_field_kernel(FormArgs a)
+__global__ __launch_bounds__(kFormThreads) void quantize_field_kernel(FormArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg, P = VEC << a.lg;
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_field_kernel(FormArg
     const int turn = lane % a.nv;
     int cg = g + turn;
     if (cg >= a.nv) cg -= a.nv;
-    auto write = [&](const uint32_t *m, int8_t *q, float *scale) {
+    auto write = [&](auto exact, const uint32_t *m, int8_t *q, float *scale) {
         I8Scale s[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s[e] = i8_scale(__uint_as_float(m[lane * VEC + e]));
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_field_kernel(FormArg
                 float w[E];
 #pragma unroll
                 for (int j = 0; j < E; ++j) w[j] = v[j][e];
-                *(u32x2 *)(lds + ((lane * VEC + e) * a.nv + cg) * 8) = i8_codes(w, s[e]);
+                *(u32x2 *)(lds + ((lane * VEC + e) * a.nv + cg) * 8) = i8_codes<decltype(exact)::value>(w, s[e]);
             }
         if (g == 0) {
             float f[VEC];
@@ -219,12 +225,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_field_kernel(FormArg
     __syncthreads();
     take(true, mx);
     __syncthreads();
-    write(mx, a.q, a.scale);
+    write(std::bool_constant<ACT == DISCO_ACT_NONE>(), mx, a.q, a.scale);
     if constexpr (ACT != DISCO_ACT_NONE)
         if (a.kq) {
             take(false, mx + P);
             __syncthreads();
-            write(mx + P, a.kq, a.kscale);
+            write(std::true_type(), mx + P, a.kq, a.kscale);
         }
 }
 
@@ -263,8 +269,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_loop_kernel(FormArgs
         load(c, v);
 #pragma unroll
         for (int j = 0; j < E; ++j) w[j] = act_value<ACT>(v[j]);
-        *(u32x2 *)(a.q + point * a.Dp + c) = i8_codes(w, s);
-        if (a.kq) *(u32x2 *)(a.kq + point * a.Dp + c) = i8_codes(v, k);
+        *(u32x2 *)(a.q + point * a.Dp + c) = i8_codes<ACT == DISCO_ACT_NONE>(w, s);
+        if (a.kq) *(u32x2 *)(a.kq + point * a.Dp + c) = i8_codes<true>(v, k);
     }
     if (g == 0) {
         a.scale[point] = s.scale;
@@ -315,7 +321,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void dequantize_rows_kernel(FormAr
 }
 
 template <typename T, int VEC>
-__global__ __launch_bounds__(kNormMaxThreads) void dequantize_field_kernel(FormArgs a)
+__global__ __launch_bounds__(kFormThreads) void dequantize_field_kernel(FormArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg, P = VEC << a.lg, half = a.nv >> 1;

@@ -27,15 +27,16 @@ namespace {
 
 enum Mode { kInRows, kInField, kWeightRows, kWeightField };
 
-template <int BU_, int BV_, int WU_, int WV_>
+template <int BU_, int BV_, int WU_, int WV_, int R_>
 struct BTile {
     static constexpr int BU = BU_, BV = BV_, WU = WU_, WV = WV_;
+    static constexpr int R = R_;                                 // r of a step
     static constexpr int kThreads = 64 * WU * WV;
     static constexpr int FU = BU / WU / 32, FV = BV / WV / 32;
-    static constexpr int kStage = (BU + BV) * kBR * 2;
+    static constexpr int kStage = (BU + BV) * R * 2;
 };
-typedef BTile<256, 256, 2, 4> BLarge;
-typedef BTile<128, 128, 2, 2> BSmall;
+typedef BTile<256, 256, 2, 4, 64> BLarge;
+typedef BTile<128, 128, 2, 2, 64> BSmall;
 
 struct BwdArgs {
     const uint16_t *gy;
@@ -46,8 +47,7 @@ struct BwdArgs {
     void *out;
     void *db;
     float *ws, *ws_db;             // weight with more than one split
-    Planes pl;                     // the points of gy (and of gx)
-    int64_t ld;                    // rows of gy
+    Planes pl, out_pl;             // gy's points or rows, and the output's
     uint32_t A, X, R;              // sizes of gy's free axis, of X's (C) and of the summed one
     int32_t Cp, na, nx, splits, steps;  // tiles; steps of a split
 };
@@ -75,9 +75,10 @@ __device__ __forceinline__ bf16x8 frag_across(const unsigned char *op, int n0, i
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+template <int R>
 __device__ __forceinline__ bf16x8 frag_along(const unsigned char *op, int n0, int r0, int lane)
 {
-    return *reinterpret_cast<const bf16x8 *>(op + bwd_along(n0 + (lane & 31), (r0 >> 3) + (lane >> 5)));
+    return *reinterpret_cast<const bf16x8 *>(op + bwd_along<R>(n0 + (lane & 31), (r0 >> 3) + (lane >> 5)));
 }
 
 template <bool F16>
@@ -110,7 +111,7 @@ __device__ __forceinline__ void form16(const u32x4 &w, float s, u32x4 &lo, u32x4
 }
 
 template <typename L, bool F16, int MODE, int ACT, bool DB>
-__global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
+__global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
 {
     typedef typename std::conditional<F16, f16_t, bf16_t>::type T;
     constexpr bool kWeight = MODE == kWeightRows || MODE == kWeightField;
@@ -119,9 +120,13 @@ __global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
     constexpr bool XU = MODE != kInField;                                    // X's axis lies together in the output
     constexpr int BA = XU ? L::BV : L::BU, BX = XU ? L::BU : L::BV;          // the tile along gy's axis and X's
     constexpr int FU = L::FU, FV = L::FV;
-    constexpr int LA = BA * kBR / 8 / L::kThreads, LX = BX * kBR / 16 / L::kThreads;
-    constexpr int kA = BA * kBR * 2;
+    constexpr int LA = BA * L::R / 8 / L::kThreads, LX = BX * L::R / 16 / L::kThreads;
+    constexpr int kA = BA * L::R * 2;
     // outputs: staged in fp32 where a factor follows (rows), or for the partial sums
+    constexpr bool kFieldFactor = MODE == kInField && ACT != DISCO_ACT_NONE;
+    constexpr int kTurn = 32 * (128 + 16) * L::WU * L::WV;          // kFieldFactor: LDS of the waves' pieces, then
+    constexpr int KN = L::BU * L::BV / 16 / L::kThreads;            // the checkpoint [BU][BV + 16], its scales [BU]
+    static_assert(!kFieldFactor || kTurn + L::BU * (L::BV + 16 + 4) <= 2 * L::kStage, "the checkpoint's tile fits the buffers");
     constexpr bool kFactor = MODE == kInRows && ACT != DISCO_ACT_NONE;
     __shared__ __attribute__((aligned(16))) unsigned char smem[2 * L::kStage];
 
@@ -140,9 +145,9 @@ __global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wu = wave % L::WU, wv = wave / L::WU;
     const uint32_t a0 = (uint32_t)ta * BA, x0 = (uint32_t)tx * BX;
-    const uint32_t r_begin = kWeight ? (uint32_t)z * (uint32_t)a.steps * kBR : 0u;
+    const uint32_t r_begin = kWeight ? (uint32_t)z * (uint32_t)a.steps * L::R : 0u;
     const uint32_t r_left = a.R - r_begin;
-    const int nk = (int)((kWeight && r_left > (uint32_t)a.steps * kBR) ? a.steps : (r_left + kBR - 1) / kBR);
+    const int nk = (int)((kWeight && r_left > (uint32_t)a.steps * L::R) ? a.steps : (r_left + L::R - 1) / L::R);
 
     f32x16 d[FU][FV], dbs;
 #pragma unroll
@@ -153,63 +158,84 @@ __global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
             for (int e = 0; e < 16; ++e) d[i][j][e] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) dbs[e] = 0.0f;
-    const bool has_db = DB && tx == 0;
+    // db: the tiles of one split and gy's tile share its steps (step t is tile t % shares), so that none is slower
+    const int db_shares = DB && a.splits > 1 ? a.nx : 1;
+    int db_turn = tx < db_shares ? tx : -1;   // steps until this tile's next share; -1: none
 
     u32x4 pa[LA], px[LX];
     float ps[LX];
+    // Where this thread's pieces lie: A's piece i is row an + i kAR (r together) or r ar + i kAR (else); X's row xr + i kXR.
+    constexpr int kAR = kAlong ? L::kThreads / (L::R / 8) : L::kThreads / (BA / 8), kXR = L::kThreads / (BX / 16);
+    const int ar = kAlong ? 8 * (tid % (L::R / 8)) : tid / (BA / 8), an = kAlong ? tid / (L::R / 8) : 8 * (tid % (BA / 8));
+    const int xr = tid / (BX / 16), xn = 16 * (tid % (BX / 16));
+    const int64_t a_stride = a.pl.template stride<kPlanes>();
+    const uint16_t *a_run = a.gy + (kAlong ? (int64_t)(a0 + an) * a_stride : a.pl.template run<kPlanes>(a0 + an < a.A ? a0 + an : 0));
+    const int8_t *x_run = a.q + x0 + xn;
+    // whether a step's pieces are all there and whole: then they are loaded as they lie, else one by one
+    const bool n_full = a0 + BA <= a.A && x0 + BX <= (uint32_t)a.Cp &&
+                        (kAlong || !kPlanes || a0 - a.pl.by_m.div(a0) * (uint32_t)a.pl.M + BA <= (uint32_t)a.pl.M);
     auto fetch = [&](int t) {
-        const uint32_t r0 = r_begin + (uint32_t)t * kBR;
+        const uint32_t r0 = r_begin + (uint32_t)t * L::R;
+        if (n_full && r0 + L::R <= a.R && (!kAlong || !kPlanes || r0 - a.pl.by_m.div(r0) * (uint32_t)a.pl.M + L::R <= (uint32_t)a.pl.M)) {
+            const uint16_t *p = kAlong ? a_run + a.pl.template run<kPlanes>(r0 + ar) : a_run + (int64_t)(r0 + ar) * a_stride;
+#pragma unroll
+            for (int i = 0; i < LA; ++i) pa[i] = load_as<false, u32x4>(p + (int64_t)i * kAR * a_stride);
+            const int8_t *x = x_run + (int64_t)(r0 + xr) * a.Cp;
+#pragma unroll
+            for (int i = 0; i < LX; ++i) {
+                px[i] = *(const u32x4 *)(x + (int64_t)i * kXR * a.Cp);
+                ps[i] = a.scale[r0 + xr + i * kXR];
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
-            const int s = i * L::kThreads + tid;
-            if constexpr (kAlong) {
-                const uint32_t n = a0 + (s >> 3), r = r0 + 8 * (s & 7);
-                pa[i] = n < a.A ? load_run<kPlanes>(a.gy, a.pl, a.ld, n, r, a.R) : u32x4{0, 0, 0, 0};
-            } else {
-                const uint32_t r = r0 + s / (BA / 8), n = a0 + 8 * (s % (BA / 8));
-                pa[i] = r < a.R ? load_run<kPlanes>(a.gy, a.pl, a.ld, r, n, a.A) : u32x4{0, 0, 0, 0};
-            }
+            const uint32_t r = r0 + ar + (kAlong ? 0 : i * kAR), n = a0 + an + (kAlong ? i * kAR : 0);
+            if constexpr (kAlong) pa[i] = n < a.A ? load_run<kPlanes>(a.gy, a.pl, n, r, a.R) : u32x4{0, 0, 0, 0};
+            else pa[i] = r < a.R ? load_run<kPlanes>(a.gy, a.pl, r, n, a.A) : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int i = 0; i < LX; ++i) {
-            const int s = i * L::kThreads + tid;
-            const uint32_t r = r0 + s / (BX / 16), c = x0 + 16 * (s % (BX / 16));
+            const uint32_t r = r0 + xr + i * kXR, c = x0 + xn;
             const bool in = r < a.R;
             px[i] = in && c < (uint32_t)a.Cp ? *(const u32x4 *)(a.q + (int64_t)r * a.Cp + c) : u32x4{0, 0, 0, 0};
             ps[i] = in ? a.scale[r] : 0.0f;
         }
     };
-    auto stage = [&](unsigned char *buf) {
-#pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            const int s = i * L::kThreads + tid;
-            if constexpr (kAlong) *(u32x4 *)(buf + bwd_along(s >> 3, s & 7)) = pa[i];
-            else *(u32x4 *)(buf + bwd_across<BA>(s / (BA / 8), 8 * (s % (BA / 8)))) = pa[i];
-        }
-#pragma unroll
-        for (int i = 0; i < LX; ++i) {
-            const int s = i * L::kThreads + tid;
-            u32x4 lo, hi;
-            form16<F16>(px[i], ps[i], lo, hi);
-            unsigned char *to = buf + kA + bwd_across<BX>(s / (BX / 16), 16 * (s % (BX / 16)));
-            *(u32x4 *)to = lo;
-            *(u32x4 *)(to + 16) = hi;
-        }
+    auto stage_a = [&](unsigned char *buf, int i) {
+        if constexpr (kAlong) *(u32x4 *)(buf + bwd_along<L::R>(an + i * kAR, tid % (L::R / 8))) = pa[i];
+        else *(u32x4 *)(buf + bwd_across<BA>(ar + i * kAR, an)) = pa[i];
     };
+    auto stage_x = [&](unsigned char *buf, int i) {
+        u32x4 lo, hi;
+        form16<F16>(px[i], ps[i], lo, hi);
+        unsigned char *to = buf + kA + bwd_across<BX>(xr + i * kXR, xn);
+        // every other eight lanes the second half first: sixteen lanes then meet all banks
+        const int turn = (tid >> 3) & 1;
+        *(u32x4 *)(to + 16 * turn) = turn ? hi : lo;
+        *(u32x4 *)(to + 16 - 16 * turn) = turn ? lo : hi;
+    };
+    // the parts of a step, X's before A's, are put down behind its products ks = 1 ..
+    constexpr int NKS = L::R / 16;
+    auto part_of = [](int q) { return q * (NKS - 1) / (LX + LA) + 1; };
     fetch(0);
-    stage(smem);
+#pragma unroll
+    for (int i = 0; i < LA; ++i) stage_a(smem, i);
+#pragma unroll
+    for (int i = 0; i < LX; ++i) stage_x(smem, i);
+    if (nk > 1) fetch(1);
     __syncthreads();
     bf16x8 ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ones[i] = __builtin_bit_cast(__bf16, (uint16_t)(F16 ? 0x3c00 : 0x3f80));
     for (int t = 0; t < nk; ++t) {
         const unsigned char *cur = smem + (t & 1) * L::kStage;
-        if (t + 1 < nk) fetch(t + 1);
+        unsigned char *next = smem + ((t + 1) & 1) * L::kStage;
 #pragma unroll
-        for (int ks = 0; ks < kBR / 16; ++ks) {
+        for (int ks = 0; ks < L::R / 16; ++ks) {
             bf16x8 fu[FU], fv[FV];
             auto of_a = [&](int n0) {
-                if constexpr (kAlong) return frag_along(cur, n0, 16 * ks, lane);
+                if constexpr (kAlong) return frag_along<L::R>(cur, n0, 16 * ks, lane);
                 else return frag_across<BA>(cur, n0, 16 * ks, lane);
             };
             auto of_x = [&](int n0) { return frag_across<BX>(cur + kA, n0, 16 * ks, lane); };
@@ -224,91 +250,121 @@ __global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
             // db: wave wu < FV sums the gradients of its columns' piece wu
             if constexpr (DB) {
                 static_assert(!DB || L::FV <= L::WU, "a wave for each piece");
-                if (has_db && wu < FV) dbs = bwd_mma<F16>(ones, wu == 0 ? fv[0] : fv[FV - 1], dbs);
+                if (db_turn == 0 && wu < FV) dbs = bwd_mma<F16>(ones, wu == 0 ? fv[0] : fv[FV - 1], dbs);
             }
+            // the next step's operands, asked for a step ago, into the other buffer between the products (behind the last
+            // step nothing reads them)
+#pragma unroll
+            for (int i = 0; i < LX; ++i)
+                if (part_of(i) == ks) stage_x(next, i);
+#pragma unroll
+            for (int i = 0; i < LA; ++i)
+                if (part_of(LX + i) == ks) stage_a(next, i);
         }
-        if (t + 1 < nk) stage(smem + ((t + 1) & 1) * L::kStage);
-        __syncthreads();
+        if constexpr (DB) db_turn = db_turn == 0 ? db_shares - 1 : db_turn - 1;
+        if (t + 2 < nk) fetch(t + 2);
+        // the other buffer is whole, and this one is read; loads in flight stay there
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        bare_barrier();
     }
+    __syncthreads();
 
     // A lane holds column v = lane % 32 and rows u = 8 (e / 4) + 4 (lane / 32) + e % 4 of each accumulator.
     const int r = lane & 31, h = lane >> 5;
     const uint32_t U = XU ? a.X : a.A, V = XU ? a.A : a.X;
     const uint32_t uw = (XU ? x0 : a0) + L::BU / L::WU * wu, vw = (XU ? a0 : x0) + L::BV / L::WV * wv;
     if constexpr (DB) {
-        if (has_db && wu < FV && h == 0) {
+        if (tx < db_shares && wu < FV && h == 0) {
             const uint32_t o = vw + 32 * wu + r;
             if (o < a.A) {
-                if (a.splits > 1) a.ws_db[(int64_t)z * a.A + o] = dbs[0];
+                if (a.splits > 1) a.ws_db[((int64_t)z * a.nx + tx) * a.A + o] = dbs[0];
                 else store_elem((T *)a.db, o, dbs[0]);
             }
         }
     }
+    unsigned char *ktile = smem + kTurn;
+    float *kscale = (float *)(ktile + L::BU * (L::BV + 16));
+    if constexpr (kFieldFactor) {   // the checkpoint's tile (points a0 .., channels x0 ..) to LDS
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int s = i * L::kThreads + tid, row = s / (L::BV / 16), c = 16 * (s % (L::BV / 16));
+            const uint32_t pt = a0 + row < U ? a0 + row : U - 1;
+            const u32x4 w = x0 + c < (uint32_t)a.Cp ? *(const u32x4 *)(a.kept + (int64_t)pt * a.Cp + x0 + c) : u32x4{0, 0, 0, 0};
+            *(u32x4 *)(ktile + row * (L::BV + 16) + c) = w;
+        }
+        for (int i = tid; i < L::BU; i += L::kThreads) kscale[i] = a.kept_scale[a0 + i < U ? a0 + i : U - 1];
+        __syncthreads();
+    }
+    // Each wave turns 32 v x UR u at a time in LDS of its own, and writes them as runs along u.
     auto each = [&](auto fp32) {
         constexpr bool kF32 = decltype(fp32)::value;
-        constexpr int ES = kF32 ? 4 : 2;
-        constexpr int UR = FU * 32 * ES > 256 ? 256 / ES : FU * 32, FP = UR / 32, PITCH = UR * ES + 16, PIECES = UR * ES / 16;
+        typedef typename std::conditional<kF32, float, T>::type S;   // as staged
+        constexpr int ES = (int)sizeof(S);
+        constexpr int ROW = kFieldFactor ? 128 : 256;
+        constexpr int UR = FU * 32 * ES > ROW ? ROW / ES : FU * 32, FP = UR / 32, PITCH = UR * ES + 16;
+        constexpr int LEN = kFactor ? 8 : 16 / ES, PIECES = UR / LEN;   // values of a lane's run, runs of a row
         static_assert(32 * PITCH * L::WU * L::WV <= 2 * L::kStage, "the pieces fit the buffers");
+        typedef typename std::conditional<kF32 && !kFactor, float, T>::type O;
+        O *base = (O *)a.out;
+        if constexpr (kF32 && !kFactor) base = a.ws + (int64_t)z * V * U;
         unsigned char *st = smem + wave * 32 * PITCH;
+        constexpr int ROWS = 32 * PIECES / 64;   // a lane's runs of a piece
+        // kFactor (u: channels, v: points): the checkpoint of a lane's runs, asked for before the piece is turned
+        u32x2 kept[kFactor ? ROWS : 1];
+        float ks[kFactor ? ROWS : 1];
 #pragma unroll
-        for (int j = 0; j < FV; ++j)
+        for (int p = 0; p < FU / FP; ++p) {
+            const uint32_t ul = uw + UR * p + lane % PIECES * LEN;
+            const RunOut<O, MODE == kInField> out(base, a.out_pl, ul, U);
 #pragma unroll
-            for (int p = 0; p < FU / FP; ++p) {
+            for (int j = 0; j < FV; ++j) {
+                if constexpr (kFactor) {
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        const uint32_t v = vw + 32 * j + i * (64 / PIECES) + lane / PIECES, at = v < V ? v : V - 1;
+                        kept[i] = *(const u32x2 *)(a.kept + (int64_t)at * a.Cp + (ul < U ? ul : 0));
+                        ks[i] = a.kept_scale[at];
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < FP; ++i)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int ur = 32 * i + 8 * g + 4 * h;
-                        float f[4];
+                        f32x4 f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[e] = d[FP * p + i][j][4 * g + e];
-                        if constexpr (MODE == kInField && ACT != DISCO_ACT_NONE) {  // u: points, v: channels
-                            const uint32_t c = vw + 32 * j + r;
+                        if constexpr (kFieldFactor) {  // u: points, v: channels
+                            const int at = L::BU / L::WU * wu + UR * p + ur;
+                            const f32x4 ksc = *(const f32x4 *)&kscale[at];
+                            const unsigned char *kb = ktile + at * (L::BV + 16) + L::BV / L::WV * wv + 32 * j + r;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t pt = uw + UR * p + ur + e, at = pt < U ? pt : U - 1;
-                                const int k = a.kept[(int64_t)at * a.Cp + (c < V ? c : V - 1)];
-                                f[e] *= act_slope<ACT>((float)k * a.kept_scale[at]);
-                            }
+                            for (int e = 0; e < 4; ++e) f[e] *= act_slope<ACT>((float)(int8_t)kb[e * (L::BV + 16)] * ksc[e]);
                         }
-                        unsigned char *to = st + r * PITCH + ur * ES;
-                        if constexpr (kF32) *(f32x4 *)to = f32x4{f[0], f[1], f[2], f[3]};
-                        else *(u32x2 *)to = u32x2{pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3])};
+                        put4<S>(st + r * PITCH + ur * ES, f);
                     }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                const uint32_t v0 = vw + 32 * j, u0 = uw + UR * p;
-                if constexpr (kFactor) {  // u: channels, v: points; eight channels a lane
-                    for (int i = 0; i < 32 * UR / 8 / 64; ++i) {
-                        const int s = i * 64 + lane, row = s / (UR / 8), c8 = 8 * (s % (UR / 8));
-                        const uint32_t pt = v0 + row, c = u0 + c8;
-                        if (pt >= V || c >= U) continue;
-                        const f32x4 x = *(const f32x4 *)(st + row * PITCH + c8 * 4), y = *(const f32x4 *)(st + row * PITCH + c8 * 4 + 16);
-                        const u32x2 k = *(const u32x2 *)(a.kept + (int64_t)pt * a.Cp + c);
-                        const float ks = a.kept_scale[pt];
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    const int row = i * (64 / PIECES) + lane / PIECES;
+                    const uint32_t v = vw + 32 * j + row;
+                    if constexpr (kFactor) {  // u: channels, v: points; eight channels a lane
+                        const unsigned char *from = st + row * PITCH + lane % PIECES * 32;
+                        const f32x4 x = *(const f32x4 *)from, y = *(const f32x4 *)(from + 16);
+                        if (v >= V || ul >= U) continue;
                         float f[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            f[e] = (e < 4 ? x[e] : y[e - 4]) * act_slope<ACT>((float)(int8_t)(k[e / 4] >> (8 * (e % 4))) * ks);
-                        const u32x4 w = {pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7])};
-                        store_run<T, false>((T *)a.out, a.pl, (int64_t)a.X, pt, c, U, w);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32 * PIECES / 64; ++i) {
-                        const int s = i * 64 + lane, row = s / PIECES, piece = s % PIECES;
-                        const u32x4 w = *(const u32x4 *)(st + row * PITCH + 16 * piece);
-                        if (v0 + row >= V) continue;
-                        const uint32_t u = u0 + piece * (16 / ES);
-                        if constexpr (kF32) store_run<float, false>(a.ws + (int64_t)z * V * U, a.pl, (int64_t)U, v0 + row, u, U, w);
-                        else if constexpr (MODE == kInField) {
-                            Planes out = a.pl;
-                            out.J = V;
-                            store_run<T, true>((T *)a.out, out, 0, v0 + row, u, U, w);
-                        } else store_run<T, false>((T *)a.out, a.pl, (int64_t)U, v0 + row, u, U, w);
+                            f[e] = (e < 4 ? x[e & 3] : y[e & 3]) * act_slope<ACT>((float)(int8_t)(kept[i][e / 4] >> (8 * (e % 4))) * ks[i]);
+                        out.put(v, u32x4{pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7])});
+                    } else {
+                        const u32x4 w = *(const u32x4 *)(st + row * PITCH + lane % PIECES * 16);
+                        if (v < V) out.put(v, w);
                     }
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
+        }
     };
     if constexpr (kFactor) each(std::true_type());
     else if (kWeight && a.splits > 1) each(std::true_type());
@@ -316,26 +372,46 @@ __global__ __launch_bounds__(L::kThreads) void linear_bwd_kernel(BwdArgs a)
 }
 
 // out = the sum over the splits of their partial sums, four neighbouring values a thread: 16 fours x 16 runs of splits a
-// workgroup, joined in LDS in a fixed order.
+// workgroup, joined in LDS in a fixed order.  The workgroups behind the first `blocks` join db.
+struct JoinArgs {
+    const float *ws, *ws_db;
+    void *out, *db;
+    int64_t n, n_db, blocks;
+    int32_t splits, splits_db;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(const float *ws, int64_t n, int splits, T *out)
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs a)
 {
     __shared__ double part[16][16][4];
+    const bool db = blockIdx.x >= a.blocks;
+    const float *ws = db ? a.ws_db : a.ws;
+    const int64_t n = db ? a.n_db : a.n;
+    const int splits = db ? a.splits_db : a.splits;
     const int t = threadIdx.x, x = t & 15, y = t >> 4;
-    const int64_t i = ((int64_t)blockIdx.x * 16 + x) * 4;
+    const int64_t i = ((blockIdx.x - (db ? a.blocks : 0)) * 16 + x) * 4;
     double s[4] = {0, 0, 0, 0};
     const int each = (splits + 15) / 16, z1 = min(splits, (y + 1) * each);
-    for (int z = y * each; z < z1; ++z)
+    if (i + 4 <= n) {
+#pragma unroll 8
+        for (int z = y * each; z < z1; ++z) {
+            const f32x4 v = load_as<false, f32x4>(ws + (int64_t)z * n + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (i + e < n) s[e] += ws[(int64_t)z * n + i + e];
+            for (int e = 0; e < 4; ++e) s[e] += v[e];
+        }
+    } else {
+        for (int z = y * each; z < z1; ++z)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) s[e] += ws[(int64_t)z * n + i + e];
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[y][x][e] = s[e];
     __syncthreads();
     if (y < 4 && i + y < n) {
         double v = 0;
         for (int k = 0; k < 16; ++k) v += part[k][x][y];
-        store_elem(out, i + y, (float)v);
+        store_elem((T *)(db ? a.db : a.out), i + y, (float)v);
     }
 }
 
@@ -351,7 +427,8 @@ BwdArgs bwd_args(const LinearBwdLaunch &l)
     a.gy = (const uint16_t *)l.gy; a.q = l.q; a.scale = l.scale; a.kept = l.kept; a.kept_scale = l.kept_scale;
     a.out = l.out; a.db = l.db; a.ws = l.workspace;
     a.ws_db = l.workspace ? l.workspace + (int64_t)l.splits * l.Co * l.C : nullptr;
-    a.pl.by_m = fast_div((uint32_t)l.M); a.pl.M = l.M; a.pl.J = l.Co; a.ld = l.Co;
+    a.pl.by_m = fast_div((uint32_t)l.M); a.pl.M = l.M; a.pl.J = l.Co; a.pl.ld = l.Co;
+    a.out_pl = a.pl; a.out_pl.J = l.C; a.out_pl.ld = l.C;   // gx's points or rows, or the rows of dw
     a.X = (uint32_t)l.C; a.Cp = (int32_t)l.Cp;
     a.splits = 1; a.steps = 0;
     return a;
@@ -367,6 +444,8 @@ hipError_t launch_mode(BwdArgs a, hipStream_t s)
     return hipGetLastError();
 }
 
+// 256 x 256 where the channels fill it and every CU has one (259200 rows, 2048 to 512: 694 us against 883; 1000 rows of 1024:
+// 37 against 25).
 template <bool F16, int MODE, int ACT>
 hipError_t input_tiles(const BwdArgs &a, hipStream_t s)
 {
@@ -417,9 +496,12 @@ hipError_t weight_typed(const LinearBwdLaunch &l, hipStream_t s)
     a.steps = p.steps;
     hipError_t e = l.M > 1 ? weight_tiles<F16, kWeightField>(l, a, s) : weight_tiles<F16, kWeightRows>(l, a, s);
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t n = l.Co * l.C;
-    join_kernel<T><<<dim3((uint32_t)ceil_div64(n, 64)), dim3(256), 0, s>>>(a.ws, n, p.splits, (T *)l.out);
-    if (l.db) join_kernel<T><<<dim3((uint32_t)ceil_div64(l.Co, 64)), dim3(256), 0, s>>>(a.ws_db, l.Co, p.splits, (T *)l.db);
+    JoinArgs j;
+    j.ws = a.ws; j.ws_db = a.ws_db; j.out = l.out; j.db = l.db;
+    j.n = l.Co * l.C; j.n_db = l.db ? l.Co : 0;
+    j.blocks = ceil_div64(j.n, 64);
+    j.splits = p.splits; j.splits_db = p.splits * p.nx;
+    join_kernel<T><<<dim3((uint32_t)(j.blocks + ceil_div64(j.n_db, 64))), dim3(256), 0, s>>>(j);
     return hipGetLastError();
 }
 

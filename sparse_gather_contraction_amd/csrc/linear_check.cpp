@@ -97,13 +97,28 @@ static void check_form(int64_t N, int64_t D, int64_t M, int esz)
 template <int N>
 static void check_across()
 {
-    std::vector<int> used(kBR * N * 2 / 16, 0);
-    for (int r = 0; r < kBR; ++r)
+    std::vector<int> used(64 * N * 2 / 16, 0);
+    for (int r = 0; r < 64; ++r)
         for (int n = 0; n < N; n += 8) {
             const int at = bwd_across<N>(r, n);
-            if (at % 16 || at < 0 || at + 16 > kBR * N * 2 || used[at / 16]++) fail("across", N, r, n, 0);
+            if (at % 16 || at < 0 || at + 16 > 64 * N * 2 || used[at / 16]++) fail("across", N, r, n, 0);
             for (int e = 0; e < 8; e += 4)  // what a transposing read takes: four elements
                 if (bwd_across<N>(r, n + e) != at + 2 * e) fail("across within a piece", N, r, n, e);
+        }
+}
+
+// Slot s is written by a direct load, read by row and piece; sixteen rows' equal pieces meet each bank (of 4 bytes, 64 of
+// them) once.
+template <int K>
+static void check_slots(int rows)
+{
+    for (int s = 0; s < rows * K / 16; ++s)
+        if (lin_at<K>(s / (K / 16), lin_piece<K>(s)) != 16 * s || lin_piece<K>(s) >= K / 16) fail("slot", rows, s, K, 0);
+    for (int r = 0; r < rows; r += 16)
+        for (int p = 0; p < K / 16; ++p) {
+            int banks = 0;
+            for (int i = 0; i < 16; ++i) banks |= 1 << (lin_at<K>(r + i, p) / 16 % 16);
+            if (banks != 0xffff) fail("banks", r, p, K, 0);
         }
 }
 
@@ -138,14 +153,10 @@ int main()
     check_across<128>();
     check_across<256>();
     for (int rows : {128, 256}) {
-        std::vector<int> used(rows * 8, 0);
-        for (int r = 0; r < rows; ++r)
-            for (int p = 0; p < 8; ++p) {
-                const int at = bwd_along(r, p);
-                if (at % 16 || at < 0 || at + 16 > rows * kBR * 2 || used[at / 16]++) fail("along", rows, r, p, 0);
-            }
-        for (int s = 0; s < rows * 4; ++s)  // slot s is written by a direct load, read by row and piece
-            if (lin_at(s >> 2, lin_piece(s)) != 16 * s) fail("slot", rows, s, 0, 0);
+        check_slots<64>(rows);
+        check_slots<128>(rows);
+        check_slots<256>(rows);
+        check_slots<512>(rows);
     }
     for (int64_t total : {1, 7, 8, 9, 255, 256, 1000, 8104}) {
         std::vector<int> met((size_t)total, 0);
@@ -164,11 +175,11 @@ int main()
         for (int64_t C : {1, 128, 129, 256, 512, 2048, 8192})
             for (int64_t Co : {1, 73, 129, 256, 2048, 8192}) {
                 const WeightPlan p = weight_plan(P, C, Co);
-                const int64_t all = ceil_div64(P, kBR);
+                const int64_t all = ceil_div64(P, 64);
                 // every split has a step, and all steps have a split; a split's first point fits 32 bits
                 if (p.splits < 1 || p.steps < 1 || (int64_t)(p.splits - 1) * p.steps >= all || (int64_t)p.splits * p.steps < all ||
-                    (int64_t)p.splits * p.steps * kBR > ((int64_t)1 << 32)) fail("splits", P, C, Co, p.splits);
-                if (weight_bytes(p, C, Co, true) != (p.splits == 1 ? 0 : (size_t)p.splits * (Co * C + Co) * 4)) fail("bytes", P, C, Co, 0);
+                    (int64_t)p.splits * p.steps * 64 > ((int64_t)1 << 32)) fail("splits", P, C, Co, p.splits);
+                if (weight_bytes(p, C, Co, true) != (p.splits == 1 ? 0 : (size_t)p.splits * (Co * C + Co * p.nx) * 4)) fail("bytes", P, C, Co, 0);
                 ++n;
             }
     printf("%d geometries checked\n", n);

@@ -25,53 +25,130 @@ __device__ __forceinline__ void lin_dma16(__amdgpu_buffer_rsrc_t r, uint32_t vof
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)l, 16, voff, 0, 0, 0);
 }
 
+// The same, and one of 4 bytes, as instructions whose landing the kernel waits for itself (wait_vm): the compiler puts a wait
+// for every direct load in flight before an LDS read of another array.  They write m0 and no other register (a kernel that
+// uses them has no other use for m0, which the compiler sets before each of its own); `l` and the descriptor are
+// uniform; the waits cover a descriptor or m0 written just before.
+typedef uint32_t rsrc4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ rsrc4_t lin_rsrc4(const void *base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    return {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b), (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xffffu)),
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void *l) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_ptr_t)l); }
+
+__device__ __forceinline__ void lin_dma16_free(rsrc4_t r, uint32_t voff, uint32_t l)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(l), "v"(voff), "s"(r) : "memory");
+}
+
+__device__ __forceinline__ void lin_dma4_free(rsrc4_t r, uint32_t voff, uint32_t l)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(l), "v"(voff), "s"(r) : "memory");
+}
+
 constexpr uint32_t kLinOob = 0x80000000u;  // beyond every buffer used here: the load gives zeros
 
-// Points of a tensor whose point axis is contiguous within planes of M, J channels a plane: element (j, g).
+// Waits until at most N of this wave's memory operations are in flight, and for all its LDS operations.
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N < 64, "a count of six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4 << 14));
+}
+
+// A barrier of the workgroup that leaves direct loads in flight (__syncthreads() waits for them all); LDS accesses stay on
+// their side of it.
+__device__ __forceinline__ void bare_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A tensor with one axis that lies together (c) and one that does not (j): element (j, c) lies at run(c) + j stride().
+// PLANES: c are points in planes of M with J channels; else rows of ld.
 struct Planes {
     FastDiv by_m;
-    int64_t M, J;
-    __device__ __forceinline__ int64_t at(int64_t j, uint32_t g) const
+    int64_t M, J, ld;
+    template <bool PLANES>
+    __device__ __forceinline__ int64_t run(uint32_t c) const
     {
-        const uint32_t n = by_m.div(g);
-        return ((int64_t)n * J + j) * M + (g - n * (uint32_t)M);
+        if (!PLANES) return c;
+        const uint32_t n = by_m.div(c);
+        return (int64_t)n * (J - 1) * M + c;   // n J M + (c - n M)
     }
-    // whether points g .. g + 7 lie in one plane
-    __device__ __forceinline__ bool whole(uint32_t g) const
+    template <bool PLANES>
+    __device__ __forceinline__ int64_t stride() const { return PLANES ? M : ld; }
+    // whether c .. c + 7 lie together below len
+    template <bool PLANES>
+    __device__ __forceinline__ bool whole(uint32_t c, uint32_t len) const
     {
-        return g - by_m.div(g) * (uint32_t)M + 8 <= (uint32_t)M;
+        return c + 8 <= len && (!PLANES || c - by_m.div(c) * (uint32_t)M + 8 <= (uint32_t)M);
     }
 };
 
-// Eight 16-bit elements (j, c .. c + 7) of a tensor whose axis c lies together, `len` long: PLANES: c are points in
-// planes, else (j, c) lies at j ld + c.  Zeros where c passes len.  Rows j are the caller's to bound.
+// Eight 16-bit elements (j, c .. c + 7), zeros where c passes len.  Rows j are the caller's to bound.
 template <bool PLANES>
-__device__ __forceinline__ u32x4 load_run(const uint16_t *base, const Planes &pl, int64_t ld, int64_t j, uint32_t c, uint32_t len)
+__device__ __forceinline__ u32x4 load_run(const uint16_t *base, const Planes &pl, int64_t j, uint32_t c, uint32_t len)
 {
-    if (c + 8 <= len && (!PLANES || pl.whole(c))) return load_as<false, u32x4>(base + (PLANES ? pl.at(j, c) : j * ld + c));
+    const uint16_t *row = base + j * pl.stride<PLANES>();
+    if (pl.whole<PLANES>(c, len)) return load_as<false, u32x4>(row + pl.run<PLANES>(c));
     u32x4 r = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (c + i < len) r[i / 2] |= (uint32_t)base[PLANES ? pl.at(j, c + i) : j * ld + c + i] << (16 * (i & 1));
+        if (c + i < len) r[i / 2] |= (uint32_t)row[pl.run<PLANES>(c + i)] << (16 * (i & 1));
     return r;
 }
 
-// Elements (v, u .. u + n-1), n = 16 / sizeof(T), of an output whose axis u lies together.
+// One lane's 16-byte pieces of an output whose axis u lies together: the places (v, u .. u + n-1), n = 16 / sizeof(T), of
+// one u and many v.
 template <typename T, bool PLANES>
-__device__ __forceinline__ void store_run(T *base, const Planes &pl, int64_t ld, int64_t v, uint32_t u, uint32_t len, const u32x4 &w)
-{
-    constexpr int n = 16 / (int)sizeof(T);
-    if (u + n <= len && (!PLANES || pl.whole(u))) {  // (eight points in a plane: more than fp32's four need)
-        store_as<false>(base + (PLANES ? pl.at(v, u) : v * ld + u), w);
-        return;
+struct RunOut {
+    T *p;
+    int64_t stride;
+    uint32_t u, len;
+    const Planes &pl;
+    bool whole;
+    __device__ __forceinline__ RunOut(T *base, const Planes &planes, uint32_t u_, uint32_t len_)
+        : p(base + planes.run<PLANES>(u_)), stride(planes.stride<PLANES>()), u(u_), len(len_), pl(planes),
+          whole(planes.whole<PLANES>(u_, len_))  // (eight points in a plane: more than fp32's four need)
+    {
     }
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-        if (u + i < len) {
-            T *p = base + (PLANES ? pl.at(v, u + i) : v * ld + u + i);
-            if constexpr (sizeof(T) == 4) *(uint32_t *)p = w[i];
-            else *(uint16_t *)p = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    __device__ __forceinline__ void put(int64_t v, const u32x4 &w) const
+    {
+        constexpr int n = 16 / (int)sizeof(T);
+        T *q = p + v * stride;
+        if (whole) {
+            store_as<false>(q, w);
+            return;
         }
+        const int64_t at0 = pl.run<PLANES>(u);
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if (u + i < len) {
+                T *to = q + (pl.run<PLANES>(u + i) - at0);
+                if constexpr (sizeof(T) == 4) *(uint32_t *)to = w[i];
+                else *(uint16_t *)to = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            }
+    }
+};
+
+// Four neighbouring values in the output's type.
+template <typename T>
+__device__ __forceinline__ void put4(unsigned char *to, const f32x4 &f)
+{
+    if constexpr (sizeof(T) == 4) {
+        *(f32x4 *)to = f;
+    } else {
+        const float v[4] = {f[0], f[1], f[2], f[3]};
+        Pack<T, 4> p;
+        pack(v, p);
+        *(u32x2 *)to = u32x2{p.w[0], p.w[1]};
+    }
 }
 
 }  // namespace disco

@@ -56,6 +56,10 @@ struct FormGeom {
 };
 
 constexpr int kFormChannels = 8;                 // channels of a thread's vector
+// Fields: workgroups of 512 threads at most, two or three of them a CU, so that the loads of one run beside the turn and the
+// stores of another (2x256x721x1440 bf16: writer 340 us, with 1024 threads and runs twice as long 407; reader 326 and 310;
+// 80x721x1440 both 108 and 123).
+constexpr int kFormThreads = 512;
 constexpr size_t kFormLds = (size_t)64 << 10;    // codes of one tile
 
 inline FormGeom form_geom(int64_t N, int64_t D, int64_t M, int esz)
@@ -81,10 +85,10 @@ inline FormGeom form_geom(int64_t N, int64_t D, int64_t M, int esz)
         g.vec = flat ? 1 : 16 / esz;
         int lg = 6;
         while (lg < 8 && (nv << lg) < 256) ++lg;
-        while (lg > 2 && ((nv << lg) > kNormMaxThreads || (((size_t)Dp * g.vec) << lg) > kFormLds)) --lg;
+        while (lg > 2 && ((nv << lg) > kFormThreads || (((size_t)Dp * g.vec) << lg) > kFormLds)) --lg;
         // shorter runs where the points would not give every CU two tiles
         while (!flat && lg > 4 && N * ceil_div64(M, (int64_t)g.vec << lg) < 512) --lg;
-        if ((nv << lg) > kNormMaxThreads || (((size_t)Dp * g.vec) << lg) > kFormLds) {
+        if ((nv << lg) > kFormThreads || (((size_t)Dp * g.vec) << lg) > kFormLds) {
             g.loop = 1;
         } else {
             g.lg = lg;
@@ -139,28 +143,33 @@ DISCO_HD void lin_tile(int64_t i, int64_t n, int32_t fast, int32_t *a, int32_t *
     *a = (int32_t)(t - (int64_t)*b * fast);
 }
 
-// LDS of a tile of 8-bit rows, 64 channels a step: slot i (16 bytes) holds row i / 4, piece lin_piece(i).  The pieces of a
-// row are turned by row / 4, so that sixteen rows' equal pieces lie in sixteen different banks.
-DISCO_HD int lin_piece(int slot) { return (slot & 3) ^ ((slot >> 4) & 3); }
-DISCO_HD int lin_at(int row, int piece) { return row * 64 + 16 * (piece ^ ((row >> 2) & 3)); }
-
-constexpr int kBR = 64;   // indices of a step of the gradients' sums
+// LDS of a tile of 8-bit rows, K channels (64 to 512) a step: slot i (16 bytes) holds row i / (K / 16), piece lin_piece(i).
+// The pieces of a row are turned by the row, so that sixteen rows' equal pieces lie in sixteen different banks.
+template <int K>
+DISCO_HD int lin_turn(int row) { return K == 64 ? row >> 2 & 3 : K == 128 ? row >> 1 & 7 : row & 15; }
+template <int K>
+DISCO_HD int lin_piece(int slot) { return (slot % (K / 16)) ^ lin_turn<K>(slot / (K / 16)); }
+template <int K>
+DISCO_HD int lin_at(int row, int piece) { return row * K + 16 * (piece ^ lin_turn<K>(row)); }
 
 // LDS of an operand staged [r][n], rows of N 16-bit elements: the 32-byte piece c of row r lies at piece
-// c ^ (r % 4 + 4 (r / 8 % 2)), so that the rows that one transposing read takes at a time meet different banks.
+// c ^ (2 (r % 4) + r / 8 % 2).  A transposing read takes rows r .. r + 3 of two neighbouring pieces, and of rows r + 8 ..
+// r + 11, at a time: these then lie in different banks.
 template <int N>
 DISCO_HD int bwd_across(int r, int n)
 {
-    return r * N * 2 + ((((n >> 4) ^ ((r & 3) | ((r >> 1) & 4))) << 5) | ((n & 15) << 1));
+    return r * N * 2 + ((((n >> 4) ^ ((r & 3) << 1 | ((r >> 3) & 1))) << 5) | ((n & 15) << 1));
 }
 
-// LDS of an operand staged [n][r], rows of 64 r: the 16-byte piece c of row n lies at piece c ^ (n / 2 % 8).
-DISCO_HD int bwd_along(int n, int piece) { return n * kBR * 2 + ((piece ^ ((n >> 1) & 7)) << 4); }
+// LDS of an operand staged [n][r], rows of R (64 or 32) r: the 16-byte pieces of a row are turned by the row.
+template <int R>
+DISCO_HD int bwd_along(int n, int piece) { return lin_at<R * 2>(n, piece); }
 
 // The weight's gradient: the points are cut into `splits` runs of `steps` steps of 64, so that the tiles of the small
 // output fill the CUs; each leaves fp32 partial sums, joined afterwards.
 struct WeightPlan {
     int32_t splits = 1, steps = 1;
+    int32_t nx = 1;            // tiles along C: they share a split's sums of db
 };
 
 inline bool weight_large(int64_t Co, int64_t C) { return Co > 128 && C > 128; }
@@ -174,6 +183,7 @@ inline WeightPlan weight_plan(int64_t P, int64_t C, int64_t Co)
     if (splits > all) splits = all;
     if (splits < 1) splits = 1;
     WeightPlan p;
+    p.nx = (int32_t)ceil_div64(C, b);
     p.steps = (int32_t)ceil_div64(all, splits);
     p.splits = (int32_t)ceil_div64(all, p.steps);
     return p;
@@ -181,7 +191,7 @@ inline WeightPlan weight_plan(int64_t P, int64_t C, int64_t Co)
 
 inline size_t weight_bytes(const WeightPlan &p, int64_t C, int64_t Co, bool bias)
 {
-    return p.splits == 1 ? 0 : (size_t)p.splits * (size_t)(Co * C + (bias ? Co : 0)) * 4;
+    return p.splits == 1 ? 0 : (size_t)p.splits * (size_t)(Co * C + (bias ? Co * p.nx : 0)) * 4;
 }
 
 }  // namespace disco
