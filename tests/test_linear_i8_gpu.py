@@ -280,3 +280,250 @@ def test_bwd_weight(points, C, Co, dt):
     assert torch.equal(dw, dw2) and db.shape == (Co,) and db.dtype == DT[dt]
     wb, sb = g.sum(0), g.abs().sum(0)
     assert bool(((db.double() - wb).abs() <= 1.01 * (sb * (P + 2) * V + u_of(dt) * wb.abs()) + SMALLEST[dt]).all())
+
+
+# ---------------------------------------------------------------- how they are called
+
+
+CALLS = {
+    "quantize": lambda s: sgc.disco_quantize_i8(s["x"], act="gelu", keep=True),
+    "dequantize": lambda s: sgc.disco_dequantize_i8(s["q"], s["s"], channels=s["C"]),
+    "linear": lambda s: sgc.disco_linear_i8(s["q"], s["s"], s["w"], s["ws"], bias=s["b"]),
+    "bwd_input": lambda s: sgc.disco_linear_i8_bwd_input(s["gy"], s["w"], s["ws"], channels=s["C"], act="gelu", kept=s["q"], kept_scale=s["s"]),
+    "bwd_weight": lambda s: sgc.disco_linear_i8_bwd_weight(s["gy"], s["q"], s["s"], channels=s["C"], bias=True),
+}
+SIZES = [((1,), 40, 50), ((100,), 256, 64), ((900,), 80, 200), ((40000,), 64, 300), ((40000,), 300, 300), ((2, 91, 181), 73, 41), ((1, 360, 128), 256, 256)]
+
+
+def state(points, C, Co, seed=0):
+    q, s, _ = form(points, C, seed + 1)
+    w, ws, _ = form((Co,), C, seed + 2, C ** -0.5)
+    return {"C": C, "x": normal(points, C, "bf16", seed + 3, 2.0), "q": q, "s": s, "w": w, "ws": ws,
+            "b": torch.randn(Co, generator=gen(seed + 4), device="cuda"), "gy": normal(points, Co, "bf16", seed + 5, 0.5)}
+
+
+def flat(r):
+    return list(r) if isinstance(r, tuple) else [r]
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("points,C,Co", SIZES, ids=str)
+def test_replays_streams_and_repeats(points, C, Co, call):
+    s, f = state(points, C, Co), CALLS[call]
+    first = flat(f(s))
+    assert all(torch.equal(a, b) for a, b in zip(first, flat(f(s))))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        there = flat(f(s))
+        here_too = flat(f(s))
+    side.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(first, there, here_too))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = flat(f(s))
+    for k in range(3):
+        t = state(points, C, Co, 100 * (k + 1))
+        for n in s:
+            if n != "C":
+                s[n].copy_(t[n])
+        eager = flat(f(t))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), k
+
+
+@pytest.mark.parametrize("points,C,Co", SIZES, ids=str)
+def test_two_streams_at_once(points, C, Co):
+    one, two = state(points, C, Co, 7), state(points, C, Co, 9)
+    want = [[flat(f(s)) for f in CALLS.values()] for s in (one, two)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for f in CALLS.values():
+        for k, s in enumerate((one, two)):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(flat(f(s)))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for a, b in zip(want[k], got[k]):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("points,C,Co", [((7,), 33, 9), ((500,), 73, 65), ((40000,), 100, 257), ((3, 9, 13), 80, 73), ((2, 91, 181), 48, 41), ((1, 360, 128), 300, 130)], ids=str)
+@pytest.mark.parametrize("dt", list(DT))
+def test_given_outputs_at_any_element_are_filled_and_nothing_beside_them(points, C, Co, dt):
+    s = state(points, C, Co)
+
+    def inside(t, skip):
+        buf = torch.full((t.numel() + 40,), 77, dtype=t.dtype, device="cuda")
+        v = buf[skip:skip + t.numel()].view(t.shape)
+        return buf, v, skip
+
+    def check(holder, want):
+        buf, v, skip = holder
+        assert torch.equal(v, want)
+        assert bool((buf[:skip] == 77).all()) and bool((buf[skip + want.numel():] == 77).all())
+
+    x = s["x"].to(DT[dt])
+    xs = inside(x, 5)
+    xs[1].copy_(x)
+    want = sgc.disco_quantize_i8(x, act="silu", keep=True)
+    outs = [inside(w, 16 if w.dtype == torch.int8 else 3) for w in want]
+    got = sgc.disco_quantize_i8(xs[1], act="silu", keep=True, q=outs[0][1], scale=outs[1][1], kept=outs[2][1], kept_scale=outs[3][1])
+    assert all(a is b[1] for a, b in zip(got, outs))
+    for o, w in zip(outs, want):
+        check(o, w)
+    want = sgc.disco_dequantize_i8(s["q"], s["s"], channels=C, dtype=DT[dt])
+    o = inside(want, 1)
+    sgc.disco_dequantize_i8(s["q"], s["s"], out=o[1], dtype=DT[dt])
+    check(o, want)
+    want = sgc.disco_linear_i8(s["q"], s["s"], s["w"], s["ws"], bias=s["b"], dtype=DT[dt])
+    o = inside(want, 1)
+    sgc.disco_linear_i8(s["q"], s["s"], s["w"], s["ws"], bias=s["b"], out=o[1], dtype=DT[dt])
+    check(o, want)
+    if dt == "f32":
+        return
+    gy = s["gy"].to(DT[dt])
+    g = inside(gy, 3)
+    g[1].copy_(gy)
+    for act in (None, "gelu"):
+        k = {} if act is None else {"act": act, "kept": s["q"], "kept_scale": s["s"]}
+        want = sgc.disco_linear_i8_bwd_input(gy, s["w"], s["ws"], channels=C, **k)
+        o = inside(want, 1)
+        sgc.disco_linear_i8_bwd_input(g[1], s["w"], s["ws"], gx=o[1], **k)
+        check(o, want)
+    want = sgc.disco_linear_i8_bwd_weight(gy, s["q"], s["s"], channels=C, bias=True)
+    outs = [inside(w, 1) for w in want]
+    need = sgc.disco_linear_i8_bwd_weight_workspace(gy, C, bias=True)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    sgc.disco_linear_i8_bwd_weight(g[1], s["q"], s["s"], dw=outs[0][1], db=outs[1][1], workspace=ws[:need] if need else None)
+    for o, w in zip(outs, want):
+        check(o, w)
+    assert bool((ws[need:] == 255).all())
+
+
+def test_refusals_on_the_device():
+    s = state((64,), 64, 64)
+    big = torch.zeros(64 * 64 + 16, dtype=torch.int8, device="cuda")
+    off = big[1:1 + 64 * 64].view(64, 64)
+    gy = normal((40000,), 64, "bf16", 1)
+    q, sc, _ = form((40000,), 64, 2)
+    small = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    for call in (lambda: sgc.disco_linear_i8(off, s["s"], s["w"], s["ws"]), lambda: sgc.disco_linear_i8(s["q"], s["s"], off, s["ws"]),
+                 lambda: sgc.disco_quantize_i8(s["x"], q=off), lambda: sgc.disco_dequantize_i8(off, s["s"]),
+                 lambda: sgc.disco_linear_i8_bwd_input(s["gy"], off, s["ws"]), lambda: sgc.disco_linear_i8_bwd_weight(s["gy"], off, s["s"]),
+                 lambda: sgc.disco_linear_i8_bwd_weight(gy, q, sc, workspace=small), lambda: sgc.disco_linear_i8(s["q"], s["s"].cpu(), s["w"], s["ws"]),
+                 lambda: sgc.disco_linear_i8_bwd_input(s["gy"], s["w"], s["ws"], gx=s["gy"]),
+                 lambda: sgc.disco_linear_i8_bwd_weight(s["gy"], s["q"], s["s"], dw=s["gy"]),
+                 lambda: sgc.disco_dequantize_i8(s["q"], s["s"], out=s["q"].view(torch.bfloat16).view(64, 32)[:, :16].contiguous().t().contiguous().t())):
+        with pytest.raises((sgc.DiscoError, ValueError)):
+            call()
+    with pytest.raises(sgc.DiscoError) as e:  # the whole of x would be overwritten as it is read
+        sgc.disco_quantize_i8(s["x"], q=s["x"].view(torch.int8)[:, :64].contiguous().view(64, 64), scale=s["x"].view(-1)[:128].view(torch.float32))
+    assert e.value.status_name == "DISCO_ERR_INVALID_ARGUMENT"
+
+
+def test_no_points():
+    q, s = torch.zeros((0, 48), dtype=torch.int8, device="cuda"), torch.zeros(0, device="cuda")
+    w, ws, _ = form((5,), 40, 1)
+    gy = torch.zeros((0, 5), dtype=torch.bfloat16, device="cuda")
+    assert sgc.disco_linear_i8(q, s, w, ws).shape == (0, 5)
+    assert sgc.disco_linear_i8_bwd_input(gy, w, ws, channels=40).shape == (0, 40)
+    assert sgc.disco_quantize_i8(torch.zeros((0, 40), device="cuda"))[0].shape == (0, 48)
+    assert sgc.disco_dequantize_i8(q, s, channels=40).shape == (0, 40)
+    dw = torch.full((5, 40), float("nan"), dtype=torch.bfloat16, device="cuda")
+    db = torch.full((5,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    sgc.disco_linear_i8_bwd_weight(gy, q, s, dw=dw, db=db)
+    assert bool((dw == 0).all()) and bool((db == 0).all())
+
+
+def test_a_nan_point_stays_its_own_in_the_input_gradient():
+    for points in ((300,), (3, 9, 13), (40000,), (1, 91, 181)):
+        gy = normal(points, 80, "bf16", 1)
+        w, ws, _ = form((80,), 260, 2)
+        k, ks, _ = form(points, 260, 3)
+        clean = rows(sgc.disco_linear_i8_bwd_input(gy, w, ws, channels=260, act="gelu", kept=k, kept_scale=ks))
+        rows_of = gy.movedim(1, -1).reshape(-1, 80)
+        bad = rows_of.clone()
+        bad[7, 3], bad[11, 79] = float("nan"), float("inf")
+        g = bad.reshape(gy.movedim(1, -1).shape).movedim(-1, 1).contiguous()
+        ks.view(-1)[20] = float("nan")   # a checkpoint that held a NaN
+        got = rows(sgc.disco_linear_i8_bwd_input(g, w, ws, channels=260, act="gelu", kept=k, kept_scale=ks))
+        hit = torch.zeros(got.shape[0], dtype=torch.bool, device="cuda")
+        hit[[7, 11, 20]] = True
+        assert torch.equal(got[~hit], clean[~hit]) and bool(torch.isnan(got[7]).all()) and bool(torch.isnan(got[20]).all())
+        assert not bool(torch.isfinite(got[11]).any())
+
+
+def test_gradients_against_differences():
+    # the product is linear in its operands' values: <gy, y(W + e D) - y(W)> / e = <dw, D>, and the same for the input
+    points, C, Co = (500,), 64, 48
+    q, s, x = form(points, C, 1)
+    w, ws, W = form((Co,), C, 2)
+    gy = normal(points, Co, "f16", 3)
+    g = rows(gy)
+    dw = sgc.disco_linear_i8_bwd_weight(gy, q, s).double()
+    gx = rows(sgc.disco_linear_i8_bwd_input(gy, w, ws))
+    y = lambda qq, ss, ww, wws: rows(sgc.disco_linear_i8(qq, ss, ww, wws, dtype=torch.float32))
+    base = y(q, s, w, ws)
+    for o, c in ((0, 0), (17, 33), (47, 63)):
+        step = 1 if int(w[o, c]) < 127 else -1
+        w2 = w.clone()
+        w2[o, c] += step
+        diff = float((g * (y(q, s, w2, ws) - base)).sum()) / (step * float(ws[o]))
+        size = float((g[:, o].abs() * x[:, c].abs()).sum())
+        # fp32 outputs: their roundings, as large as the outputs themselves; dw: fp16 operands and result
+        slack = 8 * V * float((g[:, o].abs() * base[:, o].abs()).sum()) / float(ws[o]) + 2.0 ** -11 * (size + abs(diff)) * 1.1
+        assert abs(diff - float(dw[o, c])) <= slack, (o, c)
+    for p, c in ((0, 0), (123, 45), (499, 63)):
+        step = 1 if int(q[p, c]) < 127 else -1
+        q2 = q.clone()
+        q2[p, c] += step
+        diff = float((g * (y(q2, s, w, ws) - base)).sum()) / (step * float(s[p]))
+        size = float((g[p].abs() * W[:, c].abs()).sum())
+        slack = 8 * V * float((g[p].abs() * base[p].abs()).sum()) / float(s[p]) + 2.0 ** -11 * (size + abs(diff)) * 1.1
+        assert abs(diff - float(gx[p, c])) <= slack, (p, c)
+
+
+@pytest.mark.parametrize("rows_or_field", ["rows", "field"])
+def test_elements_beyond_32_bits(rows_or_field):
+    # 2^21 + 3 points of 2064 channels: 4.3e9 codes, and as many values read and written
+    n, C, Co = (1 << 21) + 3, 2064, 32
+    shape = (n, C) if rows_or_field == "rows" else (1, C, 1, n)
+    points = (n,) if rows_or_field == "rows" else (1, 1, n)
+    x = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=gen(1))
+    q, s = sgc.disco_quantize_i8(x)
+    pick = torch.tensor([0, 1, 1 << 20, (1 << 21) - 1, n - 2, n - 1], device="cuda")
+    xr = (x[pick] if rows_or_field == "rows" else x[0, :, 0, pick].t()).float()
+    qr, sr = q.reshape(n, C)[pick], s.reshape(n)[pick]
+    want = (xr.abs().amax(1).cpu() / 127)
+    assert torch.equal(sr.cpu(), want) and torch.equal(qr.float().cpu(), torch.round(xr.cpu() / want[:, None]))
+    back = sgc.disco_dequantize_i8(q, s)
+    br = back[pick] if rows_or_field == "rows" else back[0, :, 0, pick].t()
+    assert torch.equal(br, (qr.float() * sr[:, None]).bfloat16())
+    del back, x
+    w, ws, W = form((Co,), C, 2, C ** -0.5)
+    y = sgc.disco_linear_i8(q, s, w, ws, dtype=torch.float32)
+    yr = (y[pick] if rows_or_field == "rows" else y[0, :, 0, pick].t()).double()
+    t = (qr.double() @ w.double().t()) * sr.double()[:, None] * ws.double()
+    assert bool(((yr - t).abs() <= 4.1 * V * t.abs()).all())
+    del y
+    gy = torch.zeros(points[:1] + (Co,) + points[1:], dtype=torch.bfloat16, device="cuda")
+    if rows_or_field == "rows":
+        gy[pick] = torch.randn((6, Co), generator=gen(3), device="cuda").bfloat16()
+        g = gy[pick].double()
+    else:
+        gy[0, :, 0, pick] = torch.randn((Co, 6), generator=gen(3), device="cuda").bfloat16()
+        g = gy[0, :, 0, pick].t().double()
+    xv = qr.double() * sr.double()[:, None]
+    dw = sgc.disco_linear_i8_bwd_weight(gy, q, s).double()
+    want, size = g.t() @ xv, g.abs().t() @ xv.abs()
+    assert bool(((dw - want).abs() <= 1.02 * (size * (2.0 ** -8 + 16 * V) + 2.0 ** -8 * want.abs())).all())
+    gx = sgc.disco_linear_i8_bwd_input(gy, w, ws)
+    gr = (gx[pick] if rows_or_field == "rows" else gx[0, :, 0, pick].t()).double()
+    want, size = g @ W, g.abs() @ W.abs()
+    assert bool(((gr - want).abs() <= 1.02 * (size * (2.0 ** -8 + 40 * V) + 2.0 ** -8 * want.abs())).all())
+    del gx, gy, q, s
+    torch.cuda.empty_cache()
