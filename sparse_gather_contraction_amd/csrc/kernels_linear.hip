@@ -176,7 +176,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_i8_kernel(LinArgs a)
 // ---------------------------------------------------------------- many points, up to 512 channels
 
 // The weights stay in the matrix cores' registers: a wave holds 64 output channels with all their input channels, a workgroup
-// of four 256 of them, and walks a run of points, PT at a time, which pass through a ring of tiles in LDS.
+// of four 256 of them, and walks a stream of points, PT at a time, which pass through a ring of tiles in LDS.
 template <int K_>
 struct LStay {
     static constexpr int K = K_;                        // channels, padded
@@ -189,7 +189,8 @@ constexpr int kStayChannels = 256;   // output channels of a workgroup
 
 struct StayArgs {
     LinArgs l;
-    int32_t nb, streams, tiles;      // blocks of output channels, runs of points, tiles of points
+    int32_t nt;                      // stores past the caches
+    int32_t nb, streams, tiles;      // blocks of output channels, streams, tiles of points
 };
 
 template <int KB, typename T, bool FIELD>
@@ -198,13 +199,10 @@ __global__ __launch_bounds__(256, 2) void linear_i8_stay_kernel(StayArgs a)
     typedef LStay<KB> L;
     constexpr int FX = L::PT / 32, NK = KB / 32, ES = (int)sizeof(T), RING = L::RING;
     constexpr int FU = FIELD ? FX : 2, FV = FIELD ? 2 : FX;                     // frags along u and v
-    constexpr int UR = FU * 32 * ES > 128 ? 128 / ES : FU * 32, FP = UR / 32;   // u of a staged piece
-    constexpr int PITCH = UR * ES + 16, PIECES = UR * ES / 16;
-    constexpr int NS = FU / FP * FV * (32 * PIECES / 64);                       // stores of a wave and tile
+    constexpr int NS = FU * FV * (ES == 2 ? 2 : 4);                             // stores of a wave and tile
     __shared__ __attribute__((aligned(16))) unsigned char ring[RING * L::kStage];
-    __shared__ __attribute__((aligned(16))) unsigned char turn[4 * 32 * PITCH];
     __shared__ __attribute__((aligned(16))) float factor[kStayChannels], addend[kStayChannels];
-    const int64_t me = xcd_tile(blockIdx.x, gridDim.x);   // the blocks of one run of points on one XCD
+    const int64_t me = xcd_tile(blockIdx.x, gridDim.x);   // the blocks of one stream on one XCD
     const int cb = (int)(me % a.nb), stream = (int)(me / a.nb);
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -213,7 +211,10 @@ __global__ __launch_bounds__(256, 2) void linear_i8_stay_kernel(StayArgs a)
     const uint32_t Co = FIELD ? a.l.V : a.l.U, P = FIELD ? a.l.U : a.l.V;
     const int Cp = a.l.Cp;
     const uint32_t c0 = (uint32_t)cb * kStayChannels + 64 * wave;
-    const int t_begin = (int)((int64_t)a.tiles * stream / a.streams), t_end = (int)((int64_t)a.tiles * (stream + 1) / a.streams);
+    // The streams take the tiles in turn, so that all of them write one region at a time (each a run of its own: addresses a
+    // large stride apart meet the same memory channels, 259200 rows 512 to 2048 374 against 364 us, 2076480 rows of 256 349
+    // against 298).
+    const int n_tiles = (a.tiles - stream + a.streams - 1) / a.streams;
 
     i32x4 w[2][NK];
 #pragma unroll
@@ -237,8 +238,8 @@ __global__ __launch_bounds__(256, 2) void linear_i8_stay_kernel(StayArgs a)
     }
     wait_vm<0>();   // the weights are there: no wait for them is left to the loop
     auto issue = [&](int t) {
-        unsigned char *dst = ring + (t - t_begin) % RING * L::kStage;
-        const uint32_t p0 = (uint32_t)t * L::PT;
+        unsigned char *dst = ring + t % RING * L::kStage;
+        const uint32_t p0 = (uint32_t)(stream + t * a.streams) * L::PT;
         const uint32_t left = P - p0 < (uint32_t)L::PT ? P - p0 : (uint32_t)L::PT;
         const rsrc4_t rx = lin_rsrc4(xq + (int64_t)p0 * Cp, left * (uint32_t)Cp), rs = lin_rsrc4(xsc + p0, left * 4);
         const uint32_t at = lds_offset(dst);
@@ -251,81 +252,83 @@ __global__ __launch_bounds__(256, 2) void linear_i8_stay_kernel(StayArgs a)
     };
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i)
-        if (t_begin + i < t_end) issue(t_begin + i);
-    unsigned char *st = turn + wave * 32 * PITCH;
+        if (i < n_tiles) issue(i);
     int clean = 0;   // how many of the last tiles stored NS times for certain
-    for (int t = t_begin; t < t_end; ++t) {
+    for (int t = 0; t < n_tiles; ++t) {
         // This wave's loads of tile t have landed.  What it issued after them may be in flight: the loads of the RING - 2
         // tiles that follow, and the stores of the RING - 1 tiles before this one.
-        if (t + RING - 2 >= t_end) wait_vm<0>();
+        if (t + RING - 2 >= n_tiles) wait_vm<0>();
         else if (clean == 0) wait_vm<(RING - 2) * L::LOADS>();
         else if (clean == 1) wait_vm<(RING - 2) * L::LOADS + NS>();
         else if (clean == 2 || RING == 3) wait_vm<(RING - 2) * L::LOADS + 2 * NS>();
         else wait_vm<(RING - 2) * L::LOADS + (RING - 1) * NS>();
         bare_barrier();   // everyone's have; and every wave is done with tile t - 1, whose place is filled next
-        if (t + RING - 1 < t_end) issue(t + RING - 1);
+        if (t + RING - 1 < n_tiles) issue(t + RING - 1);
         if (c0 >= Co) continue;
-        const unsigned char *cur = ring + (t - t_begin) % RING * L::kStage;
+        const unsigned char *cur = ring + t % RING * L::kStage;
         i32x16 d[FU][FV];
         const i32x16 zero = {};
+        // four of the points' operands at a time, the next four asked for before their products: alone, the compiler asks for
+        // each right before it is used and the products wait for LDS
+        constexpr int GK = 4 / FX < NK ? 4 / FX : NK, NG = NK / GK;
+        i32x4 x[2][GK][FX];
+        auto ask = [&](int g) {
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            i32x4 x[FX];
+            for (int q = 0; q < GK; ++q)
 #pragma unroll
-            for (int j = 0; j < FX; ++j) x[j] = lin_frag<KB>(cur, 32 * j + r, k, h);
+                for (int j = 0; j < FX; ++j) x[g & 1][q][j] = lin_frag<KB>(cur, 32 * j + r, g * GK + q, h);
+        };
+        ask(0);
 #pragma unroll
-            for (int j = 0; j < FX; ++j)
+        for (int g = 0; g < NG; ++g) {
+            if (g + 1 < NG) ask(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (FIELD) d[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[j], w[i][k], k ? d[j][i] : zero, 0, 0, 0);
-                    else d[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i][k], x[j], k ? d[i][j] : zero, 0, 0, 0);
-                }
+            for (int q = 0; q < GK; ++q)
+#pragma unroll
+                for (int j = 0; j < FX; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = g * GK + q;
+                        if constexpr (FIELD) d[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[g & 1][q][j], w[i][k], k ? d[j][i] : zero, 0, 0, 0);
+                        else d[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i][k], x[g & 1][q][j], k ? d[i][j] : zero, 0, 0, 0);
+                    }
+            __builtin_amdgcn_sched_barrier(0);
         }
         const float *ps = (const float *)(cur + L::kTile + 256 * wave);   // the points' scales
-        const uint32_t p0 = (uint32_t)t * L::PT;
+        const uint32_t p0 = (uint32_t)(stream + t * a.streams) * L::PT;
         const uint32_t u0 = FIELD ? p0 : c0, v0 = FIELD ? c0 : p0;
         // every lane's runs are whole and every row is there
         const bool full = p0 + L::PT <= P && c0 + 64 <= Co &&
                           (!FIELD || p0 - a.l.pl.by_m.div(p0) * (uint32_t)a.l.pl.M + L::PT <= (uint32_t)a.l.pl.M);
+        const int64_t stride = a.l.pl.template stride<FIELD>();
+        T *y = (T *)a.l.y + a.l.pl.template run<FIELD>(u0) + (int64_t)(v0 + frag_v<T, FU>(lane)) * stride + frag_u<T, FU>(lane);
 #pragma unroll
-        for (int p = 0; p < FU / FP; ++p) {
-            const RunOut<T, FIELD> out((T *)a.l.y, a.l.pl, u0 + UR * p + lane % PIECES * (16 / ES), a.l.U);
+        for (int j = 0; j < FV; ++j) {
+            const float vs = FIELD ? cs[j] : ps[32 * j + r];
+            f32x4 f[FU][4];
 #pragma unroll
-            for (int j = 0; j < FV; ++j) {
-                const float vs = FIELD ? cs[j] : ps[32 * j + r];
+            for (int i = 0; i < FU; ++i)
 #pragma unroll
-                for (int i = 0; i < FP; ++i)
+                for (int g = 0; g < 4; ++g) {
+                    const int ur = 32 * i + 8 * g + 4 * h;
+                    if constexpr (FIELD) {
+                        const f32x4 us = *(const f32x4 *)&ps[ur];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int ur = 32 * (FP * p + i) + 8 * g + 4 * h;
-                        f32x4 f;
-                        if constexpr (FIELD) {
-                            const f32x4 us = *(const f32x4 *)&ps[ur];
+                        for (int e = 0; e < 4; ++e) f[i][g][e] = (float)d[i][j][4 * g + e] * us[e] * vs + cbias[j];
+                    } else {
+                        const f32x4 us = *(const f32x4 *)&factor[64 * wave + ur], ub = *(const f32x4 *)&addend[64 * wave + ur];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = (float)d[FP * p + i][j][4 * g + e] * us[e] * vs + cbias[j];
-                        } else {
-                            const f32x4 us = *(const f32x4 *)&factor[64 * wave + ur], ub = *(const f32x4 *)&addend[64 * wave + ur];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = (float)d[FP * p + i][j][4 * g + e] * vs * us[e] + ub[e];
-                        }
-                        put4<T>(st + r * PITCH + (32 * i + 8 * g + 4 * h) * ES, f);
-                    }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                if (full) {
-#pragma unroll
-                    for (int i = 0; i < 32 * PIECES / 64; ++i) {
-                        const int row = i * (64 / PIECES) + lane / PIECES;
-                        store_as<false>(out.p + (int64_t)(v0 + 32 * j + row) * out.stride, *(const u32x4 *)(st + row * PITCH + 16 * (lane % PIECES)));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32 * PIECES / 64; ++i) {
-                        const int row = i * (64 / PIECES) + lane / PIECES;
-                        const u32x4 v = *(const u32x4 *)(st + row * PITCH + 16 * (lane % PIECES));
-                        if (v0 + 32 * j + row < a.l.V) out.put(v0 + 32 * j + row, v);
+                        for (int e = 0; e < 4; ++e) f[i][g][e] = (float)d[i][j][4 * g + e] * vs * us[e] + ub[e];
                     }
                 }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (full) {
+                if (a.nt) store_frag<T, FU, true>(y + (int64_t)(32 * j) * stride, stride, f);
+                else store_frag<T, FU, false>(y + (int64_t)(32 * j) * stride, stride, f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < FU; ++i)
+                    store_frag_part<T, FIELD>((T *)a.l.y, a.l.pl, lane, u0 + 32 * i, a.l.U, v0 + 32 * j, a.l.V, f[i]);
             }
         }
         clean = full ? clean + 1 : 0;
@@ -410,12 +413,22 @@ hipError_t launch_tiles(LinArgs a, hipStream_t s)
     return hipGetLastError();
 }
 
+// Whether runs of the output are whole sectors, and many.
+template <typename T, bool FIELD>
+bool stays_whole(const LinArgs &l)
+{
+    return stream_stores(!FIELD, (int64_t)l.U * l.V * (int64_t)sizeof(T), (FIELD ? l.pl.M : l.pl.ld) * (int64_t)sizeof(T), l.y, nullptr);
+}
+
 template <int KB, typename T, bool FIELD>
 hipError_t launch_stay(const LinArgs &l, hipStream_t s)
 {
     const int64_t P = FIELD ? l.U : l.V, Co = FIELD ? l.V : l.U;
     StayArgs a;
     a.l = l;
+    // 16 bits: a store writes whole lines (259200 rows 512 to 2048 404 -> 364 us past the caches; fp32, half a line a store,
+    // 512 to 512, 151 -> 177)
+    a.nt = sizeof(T) == 2 && stays_whole<T, FIELD>(l);
     a.nb = (int32_t)ceil_div64(Co, kStayChannels);
     a.tiles = (int32_t)ceil_div64(P, LStay<KB>::PT);
     const int64_t streams = a.nb < 512 ? 512 / a.nb : 1;   // two workgroups a CU
@@ -425,11 +438,11 @@ hipError_t launch_stay(const LinArgs &l, hipStream_t s)
 }
 
 // Which kernel: 128 points at most, each weight is read once (few).  Else, up to 512 channels and points for every stream,
-// the weights stay in registers (259200 rows, 512 to 2048, bf16: 384 us against 495 in tiles of 256 x 128); fields only from
-// 257 channels on, where the tile that their runs of points need is no longer the longer one (360x720, 512 to 2048: 491
-// against 531; but 721x1440, 256 to 256: 452 against 399, 80 to 512: 384 against 296).  Else tiles: 256 x 256 where there is
-// one for every CU and the channels are many (8192^3: 558 us against 762), 256 x 128 where there is one for every CU
-// (4x181x360 fields, 32 to 64: 14.6 against 16.9), 128 x 128 (1000 rows, 1024 to 1024: 8.6 against 13.1).
+// the weights stay in registers (259200 rows, 512 to 2048, bf16: 364 us against 495 in tiles of 256 x 128); fields where the
+// output is stored past the caches (721x1440, 80 to 512: 288 against 296 us; 2x720x1440, 256 to 256: 343 against 389), or from
+// 257 channels on (360x720, 512 to 2048: 417 against 531): else the tile's runs of points are the longer ones.  Else tiles:
+// 256 x 256 where there is one for every CU and the channels are many (8192^3: 558 us against 762), 256 x 128 where there is
+// one for every CU (4x181x360 fields, 32 to 64: 14.6 against 16.9), 128 x 128 (1000 rows, 1024 to 1024: 8.6 against 13.1).
 template <typename T, bool FIELD>
 hipError_t launch_typed(const LinearLaunch &l, const LinArgs &a, hipStream_t s)
 {
@@ -442,7 +455,7 @@ hipError_t launch_typed(const LinearLaunch &l, const LinArgs &a, hipStream_t s)
         else linear_i8_few_kernel<T, 8, FIELD><<<grid, block, 0, s>>>(a, lg);
         return hipGetLastError();
     }
-    if (l.Cp <= 512 && (!FIELD || l.Cp > 256) && l.P * ceil_div64(l.Co, kStayChannels) >= 512 * 64)
+    if (l.Cp <= 512 && (!FIELD || l.Cp > 256 || (sizeof(T) == 2 && stays_whole<T, FIELD>(a))) && l.P * ceil_div64(l.Co, kStayChannels) >= 512 * 64)
         return l.Cp <= 64 ? launch_stay<64, T, FIELD>(a, s) : l.Cp <= 128 ? launch_stay<128, T, FIELD>(a, s)
              : l.Cp <= 256 ? launch_stay<256, T, FIELD>(a, s) : launch_stay<512, T, FIELD>(a, s);
     if (l.Cp > 512 && ceil_div64(l.P, 256) * ceil_div64(l.Co, 256) >= 256) return launch_tiles<LLarge, T, FIELD>(a, s);

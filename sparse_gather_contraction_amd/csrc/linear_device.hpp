@@ -118,12 +118,13 @@ struct RunOut {
           whole(planes.whole<PLANES>(u_, len_))  // (eight points in a plane: more than fp32's four need)
     {
     }
-    __device__ __forceinline__ void put(int64_t v, const u32x4 &w) const
+    __device__ __forceinline__ void put(int64_t v, const u32x4 &w, bool nt = false) const
     {
         constexpr int n = 16 / (int)sizeof(T);
         T *q = p + v * stride;
         if (whole) {
-            store_as<false>(q, w);
+            if (nt) store_as<true>(q, w);
+            else store_as<false>(q, w);
             return;
         }
         const int64_t at0 = pl.run<PLANES>(u);
@@ -136,6 +137,112 @@ struct RunOut {
             }
     }
 };
+
+// One accumulator of the matrix cores to memory without LDS.  A lane holds column v = lane % 32 and four neighbouring rows
+// u = 8 g + 4 (lane / 32) .. of it for g = 0 .. 3; lanes exchange halves, sixteens and eights until a store writes 64 or 128
+// bytes of each v.
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// `f`: N neighbouring accumulators along u (1 or 2).  `p`: this lane's place, at frag_u<N>(lane) of their u and frag_v<N>(lane)
+// of their v; `stride`: from v to v.  Two of them make whole lines of 128 bytes of 16-bit values.
+template <typename T, int N>
+__device__ __forceinline__ int frag_u(int lane)
+{
+    if constexpr (sizeof(T) == 4) return 8 * (lane >> 4 & 1) + 4 * (lane >> 5);
+    else return 16 * (lane >> 4 & 1) + 8 * (lane >> 5) + (N == 2 ? 32 * (lane >> 3 & 1) : 0);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ int frag_v(int lane) { return sizeof(T) == 2 && N == 2 ? lane & 7 : lane & 15; }
+
+// Lanes 8 .. 15 of each sixteen of `a` and 0 .. 7 of `b` change places.
+__device__ __forceinline__ void swap8(uint32_t &a, uint32_t &b)
+{
+    const uint32_t x = (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)b, 0x128, 0xf, 0xc, false);
+    b = (uint32_t)__builtin_amdgcn_update_dpp((int)b, (int)a, 0x128, 0xf, 0x3, false);
+    a = x;
+}
+
+template <typename T, int N, bool NT>
+__device__ __forceinline__ void store_frag(T *p, int64_t stride, const f32x4 (&f)[N][4])
+{
+    if constexpr (sizeof(T) == 2) {
+        uint32_t w[N][4][2];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float v[4] = {f[n][g][0], f[n][g][1], f[n][g][2], f[n][g][3]};
+                Pack<T, 4> k;
+                pack(v, k);
+                w[n][g][0] = k.w[0];
+                w[n][g][1] = k.w[1];
+            }
+            // halves: eight u of one g in each lane (g 0 and 2 below lane 32, 1 and 3 above); then the second sixteen
+#pragma unroll
+            for (int g = 0; g < 4; g += 2)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) swap32(w[n][g][i], w[n][g + 1][i]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) swap16(w[n][g][i], w[n][g + 2][i]);
+        }
+        if constexpr (N == 2)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) swap8(w[0][g][i], w[1][g][i]);
+#pragma unroll
+        for (int g = 0; g < 4; g += 2)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                store_as<NT>(p + (8 * g + 8 * n) * stride, u32x4{w[n][g][0], w[n][g][1], w[n][g + 1][0], w[n][g + 1][1]});
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = __float_as_uint(f[n][g][i]);
+                    b[i] = __float_as_uint(f[n][g + 1][i]);
+                    swap16(a[i], b[i]);
+                }
+                store_as<NT>(p + 32 * n + 8 * g, u32x4{a[0], a[1], a[2], a[3]});
+                store_as<NT>(p + 32 * n + 8 * g + 16 * stride, u32x4{b[0], b[1], b[2], b[3]});
+            }
+    }
+}
+
+// The same, element by element, for what lies below U and V.
+template <typename T, bool PLANES>
+__device__ __forceinline__ void store_frag_part(T *base, const Planes &pl, int lane, uint32_t u0, uint32_t U, uint32_t v0, uint32_t V, const f32x4 (&f)[4])
+{
+    const uint32_t v = v0 + (lane & 31);
+    if (v >= V) return;
+    T *row = base + (int64_t)v * pl.stride<PLANES>();
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t u = u0 + 8 * g + 4 * (lane >> 5) + e;
+            if (u < U) store_elem(row, pl.run<PLANES>(u), f[g][e]);
+        }
+}
 
 // Four neighbouring values in the output's type.
 template <typename T>
