@@ -20,11 +20,12 @@ PROBE_LIB = os.path.join(PKG, "libdisco_probes.so")  # microbenchmarks of the de
 
 SOURCES = ["plan.cpp", "plan_fused.cpp", "plan_tile.cpp", "kernels_tile.hip", "disco_api.hip", "kernels_gather.hip", "kernels_staged.hip", "kernels_fused.hip",
            "kernels_fused_mfma.hip", "kernels_gemm.hip", "norm_api.hip", "kernels_norm.hip", "kernels_norm_bwd.hip",
-           "kernels_grad.hip", "linear_api.hip", "kernels_form.hip", "kernels_linear.hip", "kernels_linear_bwd.hip"]
+           "kernels_grad.hip", "linear_api.hip", "kernels_form.hip", "kernels_linear.hip", "kernels_linear_bwd.hip",
+           "kernels_linear_bwd_stay.hip"]
 # Built with unaligned memory access: their vectors lie at any element (odd sizes, views into a flat buffer),
 # and they read no LDS at less than its type's alignment.
 UNALIGNED = {"kernels_norm.hip", "kernels_norm_bwd.hip", "kernels_grad.hip", "kernels_form.hip", "kernels_linear.hip",
-             "kernels_linear_bwd.hip"}
+             "kernels_linear_bwd.hip", "kernels_linear_bwd_stay.hip"}
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

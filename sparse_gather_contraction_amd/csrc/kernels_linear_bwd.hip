@@ -53,15 +53,6 @@ struct BwdArgs {
     int32_t Cp, na, nx, splits, steps;  // tiles; steps of a split
 };
 
-template <bool F16>
-__device__ __forceinline__ f32x16 bwd_mma(bf16x8 a, bf16x8 b, f32x16 c)
-{
-    if constexpr (F16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
 // The matrix cores' operand: 32 rows n0 .., lane n0 + lane % 32 holding r = r0 + 8 (lane / 32) .. + 7.
 template <int N>
 __device__ __forceinline__ bf16x8 frag_across(const unsigned char *op, int n0, int r0, int lane)
@@ -80,21 +71,6 @@ template <int R>
 __device__ __forceinline__ bf16x8 frag_along(const unsigned char *op, int n0, int r0, int lane)
 {
     return *reinterpret_cast<const bf16x8 *>(op + bwd_along<R>(n0 + (lane & 31), (r0 >> 3) + (lane >> 5)));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    const float f[2] = {a, b};
-    if constexpr (F16) {
-        Pack<f16_t, 2> p;
-        pack(f, p);
-        return p.w[0];
-    } else {
-        Pack<bf16_t, 2> p;
-        pack(f, p);
-        return p.w[0];
-    }
 }
 
 // Sixteen 8-bit values times a scale, to 16 bits.
@@ -175,18 +151,27 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     // whether a step's pieces are all there and whole: then they are loaded as they lie, else one by one
     const bool n_full = a0 + BA <= a.A && x0 + BX <= (uint32_t)a.Cp &&
                         (kAlong || !kPlanes || a0 - a.pl.by_m.div(a0) * (uint32_t)a.pl.M + BA <= (uint32_t)a.pl.M);
+    auto step_full = [&](int t) {
+        const uint32_t r0 = r_begin + (uint32_t)t * L::R;
+        return n_full && r0 + L::R <= a.R && (!kAlong || !kPlanes || r0 - a.pl.by_m.div(r0) * (uint32_t)a.pl.M + L::R <= (uint32_t)a.pl.M);
+    };
+    auto at_a = [&](int t) {
+        const uint32_t r0 = r_begin + (uint32_t)t * L::R;
+        return kAlong ? a_run + a.pl.template run<kPlanes>(r0 + ar) : a_run + (int64_t)(r0 + ar) * a_stride;
+    };
+    auto load_a = [&](const uint16_t *p, int i) { pa[i] = load_as<false, u32x4>(p + (int64_t)i * kAR * a_stride); };
+    auto load_x = [&](uint32_t r, int i) {
+        px[i] = *(const u32x4 *)(x_run + (int64_t)(r + i * kXR) * a.Cp);
+        ps[i] = a.scale[r + i * kXR];
+    };
     auto fetch = [&](int t) {
         const uint32_t r0 = r_begin + (uint32_t)t * L::R;
-        if (n_full && r0 + L::R <= a.R && (!kAlong || !kPlanes || r0 - a.pl.by_m.div(r0) * (uint32_t)a.pl.M + L::R <= (uint32_t)a.pl.M)) {
-            const uint16_t *p = kAlong ? a_run + a.pl.template run<kPlanes>(r0 + ar) : a_run + (int64_t)(r0 + ar) * a_stride;
+        if (step_full(t)) {
+            const uint16_t *p = at_a(t);
 #pragma unroll
-            for (int i = 0; i < LA; ++i) pa[i] = load_as<false, u32x4>(p + (int64_t)i * kAR * a_stride);
-            const int8_t *x = x_run + (int64_t)(r0 + xr) * a.Cp;
+            for (int i = 0; i < LA; ++i) load_a(p, i);
 #pragma unroll
-            for (int i = 0; i < LX; ++i) {
-                px[i] = *(const u32x4 *)(x + (int64_t)i * kXR * a.Cp);
-                ps[i] = a.scale[r0 + xr + i * kXR];
-            }
+            for (int i = 0; i < LX; ++i) load_x(r0 + xr, i);
             return;
         }
 #pragma unroll
@@ -232,6 +217,10 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     for (int t = 0; t < nk; ++t) {
         const unsigned char *cur = smem + (t & 1) * L::kStage;
         unsigned char *next = smem + ((t + 1) & 1) * L::kStage;
+        // the step after the next, whole: its pieces are asked for where the next step's leave their registers
+        const bool ahead = t + 2 < nk && step_full(t + 2);
+        const uint16_t *pa2 = at_a(t + 2);
+        const uint32_t xr2 = r_begin + (uint32_t)(t + 2) * L::R + xr;
 #pragma unroll
         for (int ks = 0; ks < L::R / 16; ++ks) {
             bf16x8 fu[FU], fv[FV];
@@ -257,13 +246,19 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
             // step nothing reads them)
 #pragma unroll
             for (int i = 0; i < LX; ++i)
-                if (part_of(i) == ks) stage_x(next, i);
+                if (part_of(i) == ks) {
+                    stage_x(next, i);
+                    if (ahead) load_x(xr2, i);
+                }
 #pragma unroll
             for (int i = 0; i < LA; ++i)
-                if (part_of(LX + i) == ks) stage_a(next, i);
+                if (part_of(LX + i) == ks) {
+                    stage_a(next, i);
+                    if (ahead) load_a(pa2, i);
+                }
         }
         if constexpr (DB) db_turn = db_turn == 0 ? db_shares - 1 : db_turn - 1;
-        if (t + 2 < nk) fetch(t + 2);
+        if (t + 2 < nk && !ahead) fetch(t + 2);
         // the other buffer is whole, and this one is read; loads in flight stay there
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         bare_barrier();
@@ -470,6 +465,7 @@ hipError_t input_typed(const LinearBwdLaunch &l, hipStream_t s)
     BwdArgs a = bwd_args(l);
     a.A = (uint32_t)l.P;
     a.R = (uint32_t)l.Co;
+    if (bwd_stays(l)) return launch_linear_bwd_stay(l, a.nt != 0, s);
     return l.M > 1 ? input_act<F16, kInField>(l, a, s) : input_act<F16, kInRows>(l, a, s);
 }
 

@@ -50,6 +50,10 @@ struct LinearBwdLaunch {
     int64_t P = 0, M = 1, C = 0, Cp = 0, Co = 0;
 };
 
+// The input's gradient with the weights in registers: which calls, and the launch (nt: stores past the caches).
+bool bwd_stays(const LinearBwdLaunch &a);
+hipError_t launch_linear_bwd_stay(const LinearBwdLaunch &a, bool nt, hipStream_t stream);
+
 hipError_t launch_linear_bwd_input(const LinearBwdLaunch &a, hipStream_t stream);
 hipError_t launch_linear_bwd_weight(const LinearBwdLaunch &a, hipStream_t stream);
 

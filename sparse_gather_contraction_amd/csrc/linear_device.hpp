@@ -244,6 +244,31 @@ __device__ __forceinline__ void store_frag_part(T *base, const Planes &pl, int l
         }
 }
 
+// One 32 x 32 x 16 product of the data type (operands travel as raw 16-bit patterns).
+template <bool F16>
+__device__ __forceinline__ f32x16 bwd_mma(bf16x8 a, bf16x8 b, f32x16 c)
+{
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const float f[2] = {a, b};
+    if constexpr (F16) {
+        Pack<f16_t, 2> p;
+        pack(f, p);
+        return p.w[0];
+    } else {
+        Pack<bf16_t, 2> p;
+        pack(f, p);
+        return p.w[0];
+    }
+}
+
 // Four neighbouring values in the output's type.
 template <typename T>
 __device__ __forceinline__ void put4(unsigned char *to, const f32x4 &f)

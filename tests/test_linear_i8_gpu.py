@@ -169,7 +169,10 @@ def test_rows_of_nothing_extremes_and_what_is_not_finite():
 PRODUCTS = [((1,), 1, 1), ((1,), 512, 2048), ((5,), 16, 3), ((16,), 1000, 70), ((17,), 33, 65), ((33,), 2064, 31), ((64,), 64, 256), ((65,), 80, 73),
             ((129,), 128, 257), ((300,), 272, 130), ((1000,), 48, 300), ((16500,), 64, 1100), ((4100,), 200, 4200),
             ((1, 5, 7), 33, 20), ((3, 9, 13), 80, 73), ((2, 1, 1), 16, 8), ((5, 1, 3), 100, 40), ((7, 6, 2), 64, 130), ((1, 16, 64), 256, 256),
-            ((2, 91, 181), 73, 41), ((2, 181, 360), 48, 200)]
+            ((2, 91, 181), 73, 41), ((2, 181, 360), 48, 200),
+            # the weights in registers: rows and fields, whole and ragged planes, outputs stored past the caches and not
+            ((33000,), 500, 300), ((33001,), 100, 513), ((40000,), 17, 70), ((33000,), 512, 256), ((1, 181, 360), 300, 70), ((3, 91, 181), 400, 130),
+            ((9, 60, 61), 272, 300), ((1, 512, 1024), 80, 160), ((2, 512, 520), 33, 130), ((1, 512, 1024), 256, 128)]
 
 
 @pytest.mark.parametrize("dt", list(DT))
@@ -229,25 +232,24 @@ GRADS = [((1,), 1, 1), ((1,), 256, 256), ((5,), 16, 3), ((17,), 33, 65), ((64,),
          ((7, 6, 2), 64, 130), ((1, 16, 64), 256, 256), ((2, 91, 181), 73, 41), ((2, 181, 360), 200, 48)]
 
 
-def reach(points, n):
-    """gy of these points as a view whose surroundings are NaN: what a call reads beside it shows."""
-    whole = 1
-    for v in shape_of(points, n):
-        whole *= v
-    return whole
-
-
 def surrounded(t, before=3):
+    """t as a view whose surroundings are NaN: what a call reads beside it shows."""
     buf = torch.full((t.numel() + 64 + before,), float("nan"), dtype=t.dtype, device="cuda")
     v = buf[before:before + t.numel()].view(t.shape)
     v.copy_(t)
     return v
 
 
+# rows with the weights in registers: every bucket of output channels, ragged channels and points
+STAYS = [((33001,), 301, 8), ((33001,), 300, 64), ((33001,), 257, 72), ((20000,), 600, 128), ((16500,), 600, 200), ((16401,), 520, 256),
+         ((9000,), 1030, 264), ((9001,), 1100, 512), ((70000,), 40, 512), ((40000,), 512, 136)]
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
-@pytest.mark.parametrize("points,C,Co", GRADS, ids=str)
-def test_bwd_input(points, C, Co, dt):
-    gy = surrounded(normal(points, Co, dt, 20, 0.5))
+@pytest.mark.parametrize("points,C,Co,before", [g + (3,) for g in GRADS] + [g + (8,) for g in STAYS] + [STAYS[0] + (4,), STAYS[7] + (4,)], ids=str)
+def test_bwd_input(points, C, Co, before, dt):
+    # (the rows of gy start at 16 bytes' alignment with 8 elements before them, at none with 3 and 4)
+    gy = surrounded(normal(points, Co, dt, 20, 0.5), before)
     w, ws, W = form((Co,), C, 21, Co ** -0.5)
     k, ks, kv = form(points, C, 22, 1.5)
     g = rows(gy)
@@ -292,7 +294,8 @@ CALLS = {
     "bwd_input": lambda s: sgc.disco_linear_i8_bwd_input(s["gy"], s["w"], s["ws"], channels=s["C"], act="gelu", kept=s["q"], kept_scale=s["s"]),
     "bwd_weight": lambda s: sgc.disco_linear_i8_bwd_weight(s["gy"], s["q"], s["s"], channels=s["C"], bias=True),
 }
-SIZES = [((1,), 40, 50), ((100,), 256, 64), ((900,), 80, 200), ((40000,), 64, 300), ((40000,), 300, 300), ((2, 91, 181), 73, 41), ((1, 360, 128), 256, 256)]
+SIZES = [((1,), 40, 50), ((100,), 256, 64), ((900,), 80, 200), ((40000,), 64, 300), ((40000,), 300, 304), ((33000,), 200, 40), ((9000,), 1030, 512),
+         ((2, 91, 181), 73, 41), ((1, 360, 128), 256, 256), ((1, 181, 360), 300, 70)]
 
 
 def state(points, C, Co, seed=0):
@@ -350,7 +353,7 @@ def test_two_streams_at_once(points, C, Co):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-@pytest.mark.parametrize("points,C,Co", [((7,), 33, 9), ((500,), 73, 65), ((40000,), 100, 257), ((3, 9, 13), 80, 73), ((2, 91, 181), 48, 41), ((1, 360, 128), 300, 130)], ids=str)
+@pytest.mark.parametrize("points,C,Co", [((7,), 33, 9), ((500,), 73, 65), ((40000,), 100, 257), ((40001,), 100, 264), ((3, 9, 13), 80, 73), ((2, 91, 181), 48, 41), ((1, 360, 128), 300, 130)], ids=str)
 @pytest.mark.parametrize("dt", list(DT))
 def test_given_outputs_at_any_element_are_filled_and_nothing_beside_them(points, C, Co, dt):
     s = state(points, C, Co)
@@ -439,7 +442,7 @@ def test_no_points():
 
 
 def test_a_nan_point_stays_its_own_in_the_input_gradient():
-    for points in ((300,), (3, 9, 13), (40000,), (1, 91, 181)):
+    for points in ((300,), (3, 9, 13), (40000,), (1, 91, 181)):  # the third: weights in registers
         gy = normal(points, 80, "bf16", 1)
         w, ws, _ = form((80,), 260, 2)
         k, ks, _ = form(points, 260, 3)
