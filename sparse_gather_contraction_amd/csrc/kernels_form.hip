@@ -155,8 +155,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_rows_kernel(FormArgs
 // ---------------------------------------------------------------- fields
 
 // A workgroup: 2^lg lanes along the points, nv threads along the channels.  LDS: [P][Dp] codes, [2][P] maxima.
-template <typename T, int ACT, int VEC>
-__global__ __launch_bounds__(kFormThreads) void quantize_field_kernel(FormArgs a)
+template <typename T, int ACT, int VEC, int TH>
+__global__ __launch_bounds__(TH) void quantize_field_kernel(FormArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg, P = VEC << a.lg;
@@ -327,8 +327,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void dequantize_rows_kernel(FormAr
     }
 }
 
-template <typename T, int VEC>
-__global__ __launch_bounds__(kFormThreads) void dequantize_field_kernel(FormArgs a)
+template <typename T, int VEC, int TH>
+__global__ __launch_bounds__(TH) void dequantize_field_kernel(FormArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int t = threadIdx.x, lane = t & ((1 << a.lg) - 1), g = t >> a.lg, P = VEC << a.lg, half = a.nv >> 1;
@@ -395,7 +395,7 @@ FormArgs form_args(const FormLaunch &l, const FormGeom &g)
     return a;
 }
 
-// A field kernel's launch: its LDS may pass the 64 KiB that a kernel has without asking.
+// A field kernel's launch: 2048 channels of 32 points take a little more LDS than the 64 KiB that a kernel has without asking.
 template <typename K>
 hipError_t launch_field(K kernel, dim3 grid, dim3 block, size_t lds, hipStream_t s, const FormArgs &a)
 {
@@ -414,12 +414,14 @@ hipError_t quantize_act(const FormLaunch &l, hipStream_t s)
     const FormArgs a = form_args(l, g);
     const dim3 grid((uint32_t)g.tiles), block(g.threads);
     const size_t lds = form_lds_bytes(g, a.Dp);
+    constexpr int V = 16 / (int)sizeof(T);
     if (g.loop) quantize_loop_kernel<T, ACT><<<grid, block, lds, s>>>(a);
     else if (g.rows && g.per == 1) quantize_rows_kernel<T, ACT, 1><<<grid, block, 0, s>>>(a);
     else if (g.rows && g.per == 2) quantize_rows_kernel<T, ACT, 2><<<grid, block, 0, s>>>(a);
     else if (g.rows) quantize_rows_kernel<T, ACT, 4><<<grid, block, 0, s>>>(a);
-    else if (g.vec > 1) return launch_field(quantize_field_kernel<T, ACT, 16 / (int)sizeof(T)>, grid, block, lds, s, a);
-    else return launch_field(quantize_field_kernel<T, ACT, 1>, grid, block, lds, s, a);
+    else if (g.vec > 1 && g.threads > kFormThreads) return launch_field(quantize_field_kernel<T, ACT, V, kNormMaxThreads>, grid, block, lds, s, a);
+    else if (g.vec > 1) return launch_field(quantize_field_kernel<T, ACT, V, kFormThreads>, grid, block, lds, s, a);
+    else return launch_field(quantize_field_kernel<T, ACT, 1, kNormMaxThreads>, grid, block, lds, s, a);
     return hipGetLastError();
 }
 
@@ -438,12 +440,13 @@ hipError_t dequantize_typed(const FormLaunch &l, hipStream_t s)
     const FormArgs a = form_args(l, g);
     const dim3 grid((uint32_t)g.tiles), block(g.threads);
     const size_t lds = form_lds_bytes(g, a.Dp);
+    constexpr int V = 16 / (int)sizeof(T);
     if (g.loop) dequantize_loop_kernel<T><<<grid, block, 0, s>>>(a);
     else if (g.rows && g.per == 1) dequantize_rows_kernel<T, 1><<<grid, block, 0, s>>>(a);
     else if (g.rows && g.per == 2) dequantize_rows_kernel<T, 2><<<grid, block, 0, s>>>(a);
     else if (g.rows) dequantize_rows_kernel<T, 4><<<grid, block, 0, s>>>(a);
-    else if (g.vec > 1) return launch_field(dequantize_field_kernel<T, 16 / (int)sizeof(T)>, grid, block, lds, s, a);
-    else return launch_field(dequantize_field_kernel<T, 1>, grid, block, lds, s, a);
+    else if (g.vec > 1) return launch_field(dequantize_field_kernel<T, V, kNormMaxThreads>, grid, block, lds, s, a);
+    else return launch_field(dequantize_field_kernel<T, 1, kNormMaxThreads>, grid, block, lds, s, a);
     return hipGetLastError();
 }
 

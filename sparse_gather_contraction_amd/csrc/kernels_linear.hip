@@ -340,7 +340,6 @@ __global__ __launch_bounds__(256, 2) void linear_i8_stay_kernel(StayArgs a)
 // Up to 16 MT points against all weights, each weight read once: a workgroup takes 16 output channels, its eight waves
 // a share of the input channels each, straight from memory into the matrix cores' registers; the shares are joined in LDS
 // (whole numbers: the order does not matter).
-constexpr int kFewWaves = 8;
 constexpr int kFewSteps = 4;   // steps of 64 channels asked for in one go
 
 template <typename T, int MT, bool FIELD>
@@ -446,7 +445,7 @@ hipError_t launch_stay(const LinArgs &l, hipStream_t s)
 template <typename T, bool FIELD>
 hipError_t launch_typed(const LinearLaunch &l, const LinArgs &a, hipStream_t s)
 {
-    if (l.P <= 128) {
+    if (l.P <= kFewPoints) {
         const dim3 grid((uint32_t)ceil_div64(l.Co, 16)), block(64 * kFewWaves);
         const int lg = l.Cp >= 2048 ? 8 : 6;   // 16 rows, 8192 to 8192: 17.8 us in runs of 256 channels, 19.0 in runs of 64
         if (l.P <= 16) linear_i8_few_kernel<T, 1, FIELD><<<grid, block, 0, s>>>(a, lg);

@@ -162,7 +162,7 @@ disco_status linear_impl(const disco_tensor *q, const disco_tensor *scale, const
     if (bias && (bias->ndim != 1 || bias->shape[0] != v.D)) return api_fail(DISCO_ERR_SHAPE, "bias must be (Co,)");
     if (v.N == 0 || v.M == 0) return DISCO_OK;
     const int64_t P = v.N * v.M;
-    if ((st = check_tiles(ceil_div64(P, 128), ceil_div64(v.D, 128), 256)) != DISCO_OK) return st;
+    if ((st = check_grid(lin_blocks(P, v.D), lin_threads(P))) != DISCO_OK) return st;
     int dev = -1;
     if ((st = current_device(&dev)) != DISCO_OK) return st;
     if ((st = check_form_pointers(q, scale, "q", "scale", dev)) != DISCO_OK) return st;

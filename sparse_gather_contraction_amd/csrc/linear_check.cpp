@@ -29,7 +29,7 @@ static void check_form(int64_t N, int64_t D, int64_t M, int esz)
     const int nv = (int)(Dp / kFormChannels), lanes = 1 << g.lg;
     REQUIRE(Dp % 16 == 0 && Dp >= D && Dp < D + 16);
     REQUIRE(g.threads >= 64 && g.threads <= kNormMaxThreads && g.threads % 64 == 0 && g.tiles >= 1);
-    REQUIRE(form_lds_bytes(g, Dp) <= 80 * 1024);
+    REQUIRE(form_lds_bytes(g, Dp) <= 65 * 1024);
     std::vector<int> codes((size_t)(P * nv), 0), held((size_t)(N * D * M), 0);
     if (g.loop) {
         const int groups = g.threads >> g.lg;
@@ -141,7 +141,7 @@ int main()
                     check_form(N, D, M, esz);
                     ++n;
                 }
-        for (int64_t D : {2047, 2048, 2049, 4097, 8192, 16385, 32768, 32769, 40000}) {
+        for (int64_t D : {1024, 1025, 2032, 2047, 2048, 2049, 4097, 8192, 16385, 32768, 32769, 40000}) {
             check_form(3, D, 1, esz);
             check_form(1, D, 70, esz);
             check_form(2, D, 5, esz);

@@ -56,11 +56,10 @@ struct FormGeom {
 };
 
 constexpr int kFormChannels = 8;                 // channels of a thread's vector
-// Fields: workgroups of 512 threads at most, two or three of them a CU, so that the loads of one run beside the turn and the
-// stores of another (2x256x721x1440 bf16: writer 340 us, with 1024 threads and runs twice as long 407; reader 326 and 310;
-// 80x721x1440 both 108 and 123).
+// Fields: workgroups of 512 threads, two or three of them a CU, so that the loads of one run beside the turn and the stores
+// of another (2x256x721x1440 bf16: writer 340 us, with 1024 threads and runs twice as long 407; reader 326 and 310;
+// 80x721x1440 both 108 and 123); 1024 where that many hold the channels of a few points at least.
 constexpr int kFormThreads = 512;
-constexpr size_t kFormLds = (size_t)64 << 10;    // codes of one tile
 
 inline FormGeom form_geom(int64_t N, int64_t D, int64_t M, int esz)
 {
@@ -85,10 +84,11 @@ inline FormGeom form_geom(int64_t N, int64_t D, int64_t M, int esz)
         g.vec = flat ? 1 : 16 / esz;
         int lg = 6;
         while (lg < 8 && (nv << lg) < 256) ++lg;
-        while (lg > 2 && ((nv << lg) > kFormThreads || (((size_t)Dp * g.vec) << lg) > kFormLds)) --lg;
+        const int most = (nv << 2) > kFormThreads ? kNormMaxThreads : kFormThreads;
+        while (lg > 2 && (nv << lg) > most) --lg;
         // shorter runs where the points would not give every CU two tiles
         while (!flat && lg > 4 && N * ceil_div64(M, (int64_t)g.vec << lg) < 512) --lg;
-        if ((nv << lg) > kFormThreads || (((size_t)Dp * g.vec) << lg) > kFormLds) {
+        if ((nv << lg) > most) {
             g.loop = 1;
         } else {
             g.lg = lg;
@@ -132,6 +132,13 @@ inline size_t form_lds_bytes(const FormGeom &g, int64_t Dp)
 
 // ---- the products
 //
+constexpr int kFewPoints = 128;    // so many points at most: each weight is read once, 16 output channels a workgroup
+constexpr int kFewWaves = 8;       // of so many waves
+
+// Workgroups and their threads of a product, at most.
+inline int64_t lin_blocks(int64_t P, int64_t Co) { return P <= kFewPoints ? ceil_div64(Co, 16) : ceil_div64(P, 128) * ceil_div64(Co, 128); }
+inline int lin_threads(int64_t P) { return P <= kFewPoints ? 64 * kFewWaves : 256; }
+
 // out[v][u] over tiles of BU x BV, u the axis that lies together in the output.  The tensor that holds the
 // points may be a field: then the points' axis is cut into planes of M (plane(g) = g / M).
 

@@ -99,6 +99,8 @@ BAD = [
     (lambda: linear(axis=-1), "SHAPE", "points"),
     (lambda: linear(q=desc((1 << 30, 16), I8), scale=desc((1 << 30,), F32), w=desc((1 << 28, 16), I8), ws=desc((1 << 28,), F32),
                     y=desc((1 << 30, 1 << 28))), "SHAPE", "workgroups"),
+    (lambda: linear(q=desc((1, 16), I8), scale=desc((1,), F32), w=desc((1 << 28, 16), I8), ws=desc((1 << 28,), F32), y=desc((1, 1 << 28))),
+     "SHAPE", "workgroups"),
     (lambda: grad_x(gx=None), "INVALID_ARGUMENT", "NULL"),
     (lambda: grad_x(act=1), "INVALID_ARGUMENT", "checkpoint"),
     (lambda: grad_x(k=K, ks=KS), "INVALID_ARGUMENT", "checkpoint"),

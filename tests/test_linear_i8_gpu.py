@@ -110,7 +110,7 @@ def test_dequantize(points, dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
-@pytest.mark.parametrize("shape", [(3, 2100, 4, 70), (2, 5000, 3, 5), (4, 40000), (1, 1 << 20)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 1024, 3, 70), (1, 1030, 9, 80), (3, 2048, 4, 70), (2, 1500, 3, 5), (3, 2100, 4, 70), (2, 5000, 3, 5), (4, 40000), (1, 1 << 20)], ids=str)
 def test_long_axes(shape, dt):
     # channels beyond what a workgroup's registers or its LDS hold
     x = (torch.randn(shape, generator=gen(5), device="cuda") * 2).to(DT[dt])
