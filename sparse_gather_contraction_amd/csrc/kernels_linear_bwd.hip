@@ -37,6 +37,8 @@ struct BTile {
 };
 typedef BTile<256, 256, 2, 4, 64> BLarge;
 typedef BTile<128, 128, 2, 2, 64> BSmall;
+typedef BTile<32, 256, 1, 4, 64> BNarrowU;   // few input channels, X along u
+typedef BTile<256, 32, 4, 1, 64> BNarrowV;   // and along v
 
 struct BwdArgs {
     const uint16_t *gy;
@@ -97,7 +99,8 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     constexpr bool XU = MODE != kInField;                                    // X's axis lies together in the output
     constexpr int BA = XU ? L::BV : L::BU, BX = XU ? L::BU : L::BV;          // the tile along gy's axis and X's
     constexpr int FU = L::FU, FV = L::FV;
-    constexpr int LA = BA * L::R / 8 / L::kThreads, LX = BX * L::R / 16 / L::kThreads;
+    constexpr int LA = BA * L::R / 8 / L::kThreads, LX = (BX * L::R / 16 + L::kThreads - 1) / L::kThreads;
+    constexpr bool kXAll = BX * L::R / 16 % L::kThreads == 0;                // else the first threads have a piece of X
     constexpr int kA = BA * L::R * 2;
     // outputs: staged in fp32 where a factor follows (rows), or for the partial sums
     constexpr bool kFieldFactor = MODE == kInField && ACT != DISCO_ACT_NONE;
@@ -126,7 +129,10 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     const uint32_t r_left = a.R - r_begin;
     const int nk = (int)((kWeight && r_left > (uint32_t)a.steps * L::R) ? a.steps : (r_left + L::R - 1) / L::R);
 
-    f32x16 d[FU][FV], dbs;
+    // db: wave wu < FV sums the gradients of its columns' piece wu, or a wave alone along u all of them
+    static_assert(!DB || FV <= L::WU || L::WU == 1, "a wave for each piece");
+    constexpr int DBN = DB && FV > L::WU ? FV : 1;
+    f32x16 d[FU][FV], dbs[DBN];
 #pragma unroll
     for (int i = 0; i < FU; ++i)
 #pragma unroll
@@ -134,7 +140,9 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
 #pragma unroll
             for (int e = 0; e < 16; ++e) d[i][j][e] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dbs[e] = 0.0f;
+    for (int n = 0; n < DBN; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dbs[n][e] = 0.0f;
     // db: the tiles of one split and gy's tile share its steps (step t is tile t % shares), so that none is slower
     const int db_shares = DB && a.splits > 1 ? a.nx : 1;
     int db_turn = tx < db_shares ? tx : -1;   // steps until this tile's next share; -1: none
@@ -145,6 +153,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     constexpr int kAR = kAlong ? L::kThreads / (L::R / 8) : L::kThreads / (BA / 8), kXR = L::kThreads / (BX / 16);
     const int ar = kAlong ? 8 * (tid % (L::R / 8)) : tid / (BA / 8), an = kAlong ? tid / (L::R / 8) : 8 * (tid % (BA / 8));
     const int xr = tid / (BX / 16), xn = 16 * (tid % (BX / 16));
+    const bool has_x = kXAll || xr < L::R;
     const int64_t a_stride = a.pl.template stride<kPlanes>();
     const uint16_t *a_run = a.gy + (kAlong ? (int64_t)(a0 + an) * a_stride : a.pl.template run<kPlanes>(a0 + an < a.A ? a0 + an : 0));
     const int8_t *x_run = a.q + x0 + xn;
@@ -161,6 +170,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     };
     auto load_a = [&](const uint16_t *p, int i) { pa[i] = load_as<false, u32x4>(p + (int64_t)i * kAR * a_stride); };
     auto load_x = [&](uint32_t r, int i) {
+        if (!has_x) return;
         px[i] = *(const u32x4 *)(x_run + (int64_t)(r + i * kXR) * a.Cp);
         ps[i] = a.scale[r + i * kXR];
     };
@@ -183,7 +193,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
 #pragma unroll
         for (int i = 0; i < LX; ++i) {
             const uint32_t r = r0 + xr + i * kXR, c = x0 + xn;
-            const bool in = r < a.R;
+            const bool in = r < a.R && has_x;
             px[i] = in && c < (uint32_t)a.Cp ? *(const u32x4 *)(a.q + (int64_t)r * a.Cp + c) : u32x4{0, 0, 0, 0};
             ps[i] = in ? a.scale[r] : 0.0f;
         }
@@ -193,6 +203,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
         else *(u32x4 *)(buf + bwd_across<BA>(ar + i * kAR, an)) = pa[i];
     };
     auto stage_x = [&](unsigned char *buf, int i) {
+        if (!has_x) return;
         u32x4 lo, hi;
         form16<F16>(px[i], ps[i], lo, hi);
         unsigned char *to = buf + kA + bwd_across<BX>(xr + i * kXR, xn);
@@ -237,10 +248,11 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
             for (int i = 0; i < FU; ++i)
 #pragma unroll
                 for (int j = 0; j < FV; ++j) d[i][j] = bwd_mma<F16>(fu[i], fv[j], d[i][j]);
-            // db: wave wu < FV sums the gradients of its columns' piece wu
             if constexpr (DB) {
-                static_assert(!DB || L::FV <= L::WU, "a wave for each piece");
-                if (db_turn == 0 && wu < FV) dbs = bwd_mma<F16>(ones, wu == 0 ? fv[0] : fv[FV - 1], dbs);
+                if (db_turn == 0 && wu < FV)
+#pragma unroll
+                    for (int n = 0; n < DBN; ++n)
+                        dbs[n] = bwd_mma<F16>(ones, DBN > 1 ? fv[n] : wu == 0 ? fv[0] : fv[FV - 1], dbs[n]);
             }
             // the next step's operands, asked for a step ago, into the other buffer between the products (behind the last
             // step nothing reads them)
@@ -270,13 +282,15 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_bwd_kernel(BwdArgs a)
     const uint32_t U = XU ? a.X : a.A, V = XU ? a.A : a.X;
     const uint32_t uw = (XU ? x0 : a0) + L::BU / L::WU * wu, vw = (XU ? a0 : x0) + L::BV / L::WV * wv;
     if constexpr (DB) {
-        if (tx < db_shares && wu < FV && h == 0) {
-            const uint32_t o = vw + 32 * wu + r;
-            if (o < a.A) {
-                if (a.splits > 1) a.ws_db[((int64_t)z * a.nx + tx) * a.A + o] = dbs[0];
-                else store_elem((T *)a.db, o, dbs[0]);
+        if (tx < db_shares && wu < FV && h == 0)
+#pragma unroll
+            for (int n = 0; n < DBN; ++n) {
+                const uint32_t o = vw + 32 * (DBN > 1 ? n : wu) + r;
+                if (o < a.A) {
+                    if (a.splits > 1) a.ws_db[((int64_t)z * a.nx + tx) * a.A + o] = dbs[n][0];
+                    else store_elem((T *)a.db, o, dbs[n][0]);
+                }
             }
-        }
     }
     unsigned char *ktile = smem + kTurn;
     float *kscale = (float *)(ktile + L::BU * (L::BV + 16));
@@ -448,6 +462,7 @@ template <bool F16, int MODE, int ACT>
 hipError_t input_tiles(const BwdArgs &a, hipStream_t s)
 {
     if (a.X > 128 && ceil_div64(a.A, 256) * ceil_div64(a.X, 256) >= 256) return launch_mode<BLarge, F16, MODE, ACT, false>(a, s);
+    if (a.X <= kNarrow) return launch_mode<typename std::conditional<MODE == kInField, BNarrowV, BNarrowU>::type, F16, MODE, ACT, false>(a, s);
     return launch_mode<BSmall, F16, MODE, ACT, false>(a, s);
 }
 
@@ -474,6 +489,8 @@ hipError_t weight_tiles(const LinearBwdLaunch &l, const BwdArgs &a, hipStream_t 
 {
     if (weight_large(l.Co, l.C))
         return l.db ? launch_mode<BLarge, F16, MODE, DISCO_ACT_NONE, true>(a, s) : launch_mode<BLarge, F16, MODE, DISCO_ACT_NONE, false>(a, s);
+    if (l.C <= kNarrow)
+        return l.db ? launch_mode<BNarrowU, F16, MODE, DISCO_ACT_NONE, true>(a, s) : launch_mode<BNarrowU, F16, MODE, DISCO_ACT_NONE, false>(a, s);
     return l.db ? launch_mode<BSmall, F16, MODE, DISCO_ACT_NONE, true>(a, s) : launch_mode<BSmall, F16, MODE, DISCO_ACT_NONE, false>(a, s);
 }
 

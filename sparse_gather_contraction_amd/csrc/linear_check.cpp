@@ -150,6 +150,7 @@ int main()
     }
     check_form(700, 256, 1, 2);
     check_form(1, 64, 66000, 2);  // tiles of the whole run
+    check_across<32>();
     check_across<128>();
     check_across<256>();
     for (int rows : {128, 256}) {
@@ -172,7 +173,7 @@ int main()
             if (v != 1) fail("tile met", total, v, 0, 0);
     }
     for (int64_t P : {(int64_t)1, (int64_t)63, (int64_t)64, (int64_t)65, (int64_t)1000, (int64_t)16400, (int64_t)70000, (int64_t)259200, (int64_t)2076480, kMaxPoints})
-        for (int64_t C : {1, 128, 129, 256, 512, 2048, 8192})
+        for (int64_t C : {1, 32, 33, 128, 129, 256, 512, 2048, 8192})
             for (int64_t Co : {1, 73, 129, 256, 2048, 8192}) {
                 const WeightPlan p = weight_plan(P, C, Co);
                 const int64_t all = ceil_div64(P, 64);

@@ -165,7 +165,8 @@ DISCO_HD int lin_at(int row, int piece) { return row * K + 16 * (piece ^ lin_tur
 template <int N>
 DISCO_HD int bwd_across(int r, int n)
 {
-    return r * N * 2 + ((((n >> 4) ^ ((r & 3) << 1 | ((r >> 3) & 1))) << 5) | ((n & 15) << 1));
+    const int turn = N >= 128 ? (r & 3) << 1 | ((r >> 3) & 1) : 0;   // (N = 32: four rows are 256 bytes as they lie)
+    return r * N * 2 + ((((n >> 4) ^ turn) << 5) | ((n & 15) << 1));
 }
 
 // LDS of an operand staged [n][r], rows of R (64 or 32) r: the 16-byte pieces of a row are turned by the row.
@@ -179,18 +180,21 @@ struct WeightPlan {
     int32_t nx = 1;            // tiles along C: they share a split's sums of db
 };
 
+// Tiles of the gradients: 256 x 256, 128 x 128, or for 32 input channels at most 32 of them x 256.
+constexpr int kNarrow = 32;
 inline bool weight_large(int64_t Co, int64_t C) { return Co > 128 && C > 128; }
 
 inline WeightPlan weight_plan(int64_t P, int64_t C, int64_t Co)
 {
-    const bool large = weight_large(Co, C);
-    const int64_t b = large ? 256 : 128, tiles = ceil_div64(C, b) * ceil_div64(Co, b);
+    const bool large = weight_large(Co, C), narrow = C <= kNarrow;
+    const int64_t bx = large ? 256 : narrow ? kNarrow : 128, ba = large || narrow ? 256 : 128;
+    const int64_t tiles = ceil_div64(C, bx) * ceil_div64(Co, ba);
     const int64_t all = ceil_div64(P, 64), want = large ? 256 : 512;   // workgroups: one or two a CU
     int64_t splits = want / tiles;
     if (splits > all) splits = all;
     if (splits < 1) splits = 1;
     WeightPlan p;
-    p.nx = (int32_t)ceil_div64(C, b);
+    p.nx = (int32_t)ceil_div64(C, bx);
     p.steps = (int32_t)ceil_div64(all, splits);
     p.splits = (int32_t)ceil_div64(all, p.steps);
     return p;

@@ -229,7 +229,9 @@ def test_linear_nan_point_and_channel(points):
 
 GRADS = [((1,), 1, 1), ((1,), 256, 256), ((5,), 16, 3), ((17,), 33, 65), ((64,), 64, 256), ((65,), 80, 73), ((129,), 128, 257), ((300,), 272, 130),
          ((1000,), 48, 300), ((33000,), 300, 40), ((1, 5, 7), 33, 20), ((3, 9, 13), 80, 73), ((2, 1, 1), 16, 8), ((5, 1, 3), 100, 40),
-         ((7, 6, 2), 64, 130), ((1, 16, 64), 256, 256), ((2, 91, 181), 73, 41), ((2, 181, 360), 200, 48)]
+         ((7, 6, 2), 64, 130), ((1, 16, 64), 256, 256), ((2, 91, 181), 73, 41), ((2, 181, 360), 200, 48),
+         # 32 input channels at most: tiles of their own
+         ((3000,), 8, 307), ((2001,), 32, 600), ((3, 61, 67), 8, 307), ((2, 40, 64), 30, 512), ((1, 128, 64), 1, 33)]
 
 
 def surrounded(t, before=3):
