@@ -12,7 +12,11 @@
 // Tile: BU x BV outputs, steps of 64 r.  X is staged [r][c] and read through the transposing LDS read.  gy comes in either
 // order: with r together (rows for gx, fields for dw) it is staged [.][r] and read as it lies, else [r][.] and transposed as
 // X is.  Operands pass through registers (they need converting, or lie at any element), the next step's while this one is
-// multiplied; two LDS buffers.
+// multiplied; two LDS buffers.  Each part of a step is converted and put down between the products of the step before, and
+// the same part of the step after it asked for at once, so that vector instructions, LDS writes and loads run beside the
+// matrix cores (8192^3 bf16 1.02 PFLOP/s; 259200 points 512 to 2048 0.84; all at a step's end: 0.78).  Large outputs are
+// bound by the matrix cores and these together, outputs of one tile (256 x 256 at 2076480 points: 409 us, 3.9 TB/s) by the one
+// step of loads that the registers leave room for.
 #include <algorithm>
 #include <type_traits>
 
