@@ -6,7 +6,8 @@
 // Everything between the load and q is fp32, the quotient by the scale as it is stored, so that q scale is the nearest
 // such value to v (values of an activation function: by the product with the reciprocal).  Memory bounds the plain writer and
 // the reader (2x256x721x1440 bf16: 300-316 and 343 us, 5.3 and 4.7 TB/s; rows of 2048 bf16 read back at 6.1), the vector units
-// the writer with gelu and a checkpoint (259200x2048: 389-470 us).  A point that holds a NaN or an infinity has scale NaN and q 0: what is computed from it is NaN.
+// the writer with gelu and a checkpoint (259200x2048: 389-481 us).  A point that holds a NaN or an infinity has scale NaN
+// and q 0: what is computed from it is NaN.
 #include <type_traits>
 
 #include "act_device.hpp"

@@ -169,7 +169,7 @@ DISCO_HD int bwd_across(int r, int n)
     return r * N * 2 + ((((n >> 4) ^ turn) << 5) | ((n & 15) << 1));
 }
 
-// LDS of an operand staged [n][r], rows of R (64 or 32) r: the 16-byte pieces of a row are turned by the row.
+// LDS of an operand staged [n][r], rows of R (64) r: the 16-byte pieces of a row are turned by the row.
 template <int R>
 DISCO_HD int bwd_along(int n, int piece) { return lin_at<R * 2>(n, piece); }
 
