@@ -199,10 +199,12 @@ hipError_t launch_typed(int act, const GStayArgs &a, hipStream_t s)
 
 }  // namespace
 
-// Rows of whole 16-byte pieces, and a tile for every stream.
+// Rows of whole 16-byte pieces, and a tile for every stream.  A tile's checkpoints (64 points) lie behind one 32-bit size and
+// offset: longer rows than 2^24 go to the tiles, whose offsets have 64 bits.
 bool bwd_stays(const LinearBwdLaunch &l)
 {
-    return l.M == 1 && l.Co <= 512 && l.Co % 8 == 0 && ((uintptr_t)l.gy & 15) == 0 && l.P * ceil_div64(l.C, 256) >= 512 * 64;
+    return l.M == 1 && l.Co <= 512 && l.Co % 8 == 0 && ((uintptr_t)l.gy & 15) == 0 && l.P * ceil_div64(l.C, 256) >= 512 * 64 &&
+           (!l.kept || l.Cp <= 1 << 24);
 }
 
 hipError_t launch_linear_bwd_stay(const LinearBwdLaunch &l, bool nt, hipStream_t s)

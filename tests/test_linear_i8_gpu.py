@@ -532,3 +532,26 @@ def test_elements_beyond_32_bits(rows_or_field):
     assert bool(((gr - want).abs() <= 1.02 * (size * (2.0 ** -8 + 40 * V) + 2.0 ** -8 * want.abs())).all())
     del gx, gy, q, s
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("C", [1 << 24, (1 << 25) + 16, 1 << 26])
+def test_bwd_input_checkpoint_rows_beyond_32_bits(C):
+    # 64 points' checkpoints of 2^30 to 2^32 bytes: past 31 bits they fit no tile's offsets
+    n, Co = 64, 8
+    kept = torch.randint(-127, 128, (n, C), generator=gen(1), device="cuda", dtype=torch.int8)
+    ks = torch.rand(n, generator=gen(2), device="cuda") * 0.03 + 0.001
+    w = torch.randint(-127, 128, (Co, C), generator=gen(3), device="cuda", dtype=torch.int8)
+    ws = torch.rand(Co, generator=gen(4), device="cuda") * 0.01 + 0.001
+    gy = torch.randn((n, Co), generator=gen(5), device="cuda").bfloat16()
+    gx = sgc.disco_linear_i8_bwd_input(gy, w, ws, act="gelu", kept=kept, kept_scale=ks)
+    pick = torch.tensor([0, 1, 255, 256, C // 2 - 1, C // 2, C - 257, C - 1], device="cuda")
+    a = kept[:, pick].double() * ks.double()[:, None]
+    slope = 0.5 * (1 + torch.erf(a / 2 ** 0.5)) + a * torch.exp(-a * a / 2) / (2 * torch.pi) ** 0.5
+    wv, g = w[:, pick].double() * ws.double()[:, None], gy.double()
+    t, size = g @ wv, g.abs() @ wv.abs()
+    want = slope * t
+    # the weights' rounding to bf16 and the fp32 sum of 8 terms, the slope (5.1e-7 and its argument's rounding), the result
+    bar = 1.02 * (slope.abs() * size * (2.0 ** -8 + 40 * V) + 8e-7 * size + 2.0 ** -8 * want.abs())
+    assert bool(((gx[:, pick].double() - want).abs() <= bar).all())
+    del kept, w, gx
+    torch.cuda.empty_cache()
