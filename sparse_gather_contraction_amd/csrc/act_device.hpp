@@ -39,32 +39,13 @@ __device__ __forceinline__ float gelu(float v)
     return __builtin_fmaf(-__builtin_fabsf(v), n.e * n.p, __builtin_elementwise_maximum(v, 0.0f));
 }
 
-// 1/2 + an odd function h of v, as v times a polynomial in v^2 on [-L, L], 1/2 + h(L) = 1 beyond.  The coefficients are a
-// least-maximum fit of h(v) / v over t = 2 v^2 / L^2 - 1 in fp64, subject to the value at L; a NaN stays one.  With the last
-// product rounded before the sum (no fma) the ends are 0 and 1 exactly.  In fp32 arithmetic off by 5.1e-7 at most, anywhere.
-template <int N>
-__device__ __forceinline__ float half_and_odd(float v, float L, float scale, const float (&c)[N])
-{
-#pragma clang fp contract(off)
-    const float x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(v, L), -L);
-    const float t = __builtin_fmaf(x * x, scale, -1.0f);
-    float p = c[N - 1];
-#pragma unroll
-    for (int i = N - 2; i >= 0; --i) {
-        float k = c[i];
-        asm("" : "+s"(k));   // in a scalar register: as a literal, a quarter of the sums would take a move of their own
-        p = __builtin_fmaf(p, t, k);
-    }
-    const float h = p * x;
-    return h + 0.5f;
-}
-
+// Phi(v) + v phi(v): at -t e^(-t^2/2) (R(t) - t / sqrt(2 pi)), at t one less that.  The difference is R's error away from 0 at its
+// one zero (t = 0.752), and as good as R where the tail is small.
 __device__ __forceinline__ float gelu_slope(float v)
 {
-    constexpr float c[16] = {0.125845447f, -0.0639348626f, 0.0513828993f, -0.0502946228f, 0.0556100719f, -0.0642657354f, 0.0726433396f,
-                             -0.0718892291f, 0.0596861281f, -0.0565041192f, 0.0597264618f, -0.03331545f, 0.00105434807f,
-                             -0.00697237113f, 0.0174371265f, -0.00732053956f};
-    return half_and_odd(v, 5.625f, 0.06320988f, c);
+    const NormalTail n = normal_tail(v);
+    const float z = n.e * __builtin_fmaf(n.t, -0.3989422804014327f, n.p);
+    return v < 0.0f ? z : 1.0f - z;
 }
 
 __device__ __forceinline__ float logistic(float v)

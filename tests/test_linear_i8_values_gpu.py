@@ -38,3 +38,28 @@ def test_gelu_of_points_in_the_lower_tail(layout, C, dt):
     want = g.abs().amax(1) / 127
     assert bool(((s - want).abs() <= err.amax(1) / 127 + V * want * 1.01).all())
     assert bool(((q * s[:, None] - g).abs() <= s[:, None] * (0.5 + 128 * V) + err).all())
+
+
+@pytest.mark.parametrize("layout", ["rows", "field", "rows_narrow", "field_narrow", "rows_stay"])
+def test_gelu_slope_in_the_lower_tail(layout):
+    # gy w = 1 in one term, so the gradient is the slope at the kept values: -12 .. -0.76 in every channel, and their negatives
+    P, C = (40000, 257) if layout == "rows_stay" else (1000, 20 if "narrow" in layout else 129)
+    Co = 8
+    ks = (torch.arange(P, device="cuda") % 1000 + 64) * (12 / 1064 / 127)
+    k = torch.randint(-127, -125, (P, -(-C // 16) * 16), generator=gen(1), device="cuda", dtype=torch.int8)
+    k[P // 2:] *= -1
+    w, ws = torch.zeros((Co, k.shape[1]), dtype=torch.int8, device="cuda"), torch.ones(Co, device="cuda")
+    w[3] = 1
+    gy = torch.zeros((P, Co), dtype=torch.bfloat16, device="cuda")
+    gy[:, 3] = 1
+    kept, kept_scale = (k, ks) if layout.startswith("rows") else (k.view(2, 1, P // 2, -1), ks.view(2, 1, P // 2))
+    gx = rows(sgc.disco_linear_i8_bwd_input(points_as(gy, layout.split("_")[0]), w, ws, channels=C, act="gelu", kept=kept, kept_scale=kept_scale))
+    v = (k[:, :C].float() * ks[:, None]).double()   # rounded to fp32 as the kernels do
+    t = v.abs()
+    R = torch.special.erfcx(t / 2 ** 0.5) / 2
+    e, d = torch.exp(-t * t / 2), t / (2 * torch.pi) ** 0.5
+    z = e * (R - d)                                  # the slope at -t; at t it is 1 - z
+    want = torch.where(v < 0, z, 1 - z)
+    # R - t / sqrt(2 pi): the polynomial, six of its last steps and of the difference; the exponential and two products
+    err = e * (9.1e-8 * (1 + t * t / 8) * R + 8 * V * (R + d)) + z.abs() * V * (1.5 * t * t + 6) + V * want.abs() * (v > 0)
+    assert bool(((gx - want).abs() <= (err + u_of("bf16") * want.abs()) * 1.01).all())
