@@ -4,12 +4,9 @@
 //   v = act(x);  scale = max(max |v| / 127, 2^-126) over a point's channels;  q = v / scale to whole numbers (ties to even)
 //
 // Everything between the load and q is fp32, the quotient by the scale as it is stored, so that q scale is the nearest
-// such value to v (values of an activation function: by the product with the reciprocal).  Memory bounds the plain writer and
-// the reader (2x256x721x1440 bf16: 300-316 and 343 us, 5.3 and 4.7 TB/s; rows of 2048 bf16 read back at 6.1), the vector units
-// the writer with gelu and a checkpoint (259200x2048: 389-481 us).  A point that holds a NaN or an infinity has scale NaN
-// and q 0: what is computed from it is NaN.
-#include <type_traits>
-
+// such value to v.  Memory bounds the plain writer and the reader (2x256x721x1440 bf16: 300-316 and 343 us, 5.3 and 4.7 TB/s; rows
+// of 2048 bf16 read back at 6.1), the vector units the writer with gelu and a checkpoint (259200x2048: 389-481 us).  A point that
+// holds a NaN or an infinity has scale NaN and q 0: what is computed from it is NaN.
 #include "act_device.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
@@ -32,30 +29,28 @@ struct FormArgs {
     FastDiv by_half;   // nv / 2 sixteens of a point
 };
 
-// A point's scale, and what takes its values to their quotients: the product with the reciprocal, its remainder brought in
-// (off by 2^-45 before its one rounding).
+// A point's scale and its reciprocal in two parts, the first rounded correctly but for rare ties.  A quotient is the product with
+// both, v inv + v low, off by 2^-46 before its one rounding (2^-28 for scales above 2^100, whose second part is subnormal).
 struct I8Scale {
-    float scale, inv, back;
+    float scale, inv, low;
 };
 
 __device__ __forceinline__ I8Scale i8_scale(float amax)
 {
     if (!(amax < __builtin_inff())) return {__builtin_nanf(""), 0.0f, 0.0f};
     const float s = __builtin_fmaxf(amax / 127.0f, 0x1p-126f), r = __builtin_amdgcn_rcpf(s);
-    return {s, __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r), s};   // the reciprocal, rounded correctly but for rare ties
+    const float inv = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+    return {s, inv, __builtin_fmaf(-s, inv, 1.0f) * inv};
 }
 
-// Eight values to whole numbers in a byte each.  Added to 1.5 2^23 a quotient is rounded to a whole number (ties to even)
-// whose two's complement is the sum's low bits; |v / scale| <= 127 (1 + 2^-22), so none leaves a byte.
-// EXACT: the fp32 quotient.  Else (values of an activation function, which are off by more themselves) the product with the
-// rounded reciprocal, rounded once with that sum: within 127 2^-24 of the quotient.
-template <bool EXACT>
+// Eight values to whole numbers in a byte each: the fp32 quotient by the scale as it is stored.  Added to 1.5 2^23 it is rounded
+// to a whole number (ties to even) whose two's complement is the sum's low bits; |v / scale| <= 127 (1 + 2^-22), so none
+// leaves a byte.
 __device__ __forceinline__ u32x2 i8_codes(const float (&v)[E], const I8Scale &s)
 {
     uint32_t b[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        b[i] = __float_as_uint(EXACT ? f8_quot(v[i], s.inv, s.back) + 12582912.0f : __builtin_fmaf(v[i], s.inv, 12582912.0f));
+    for (int i = 0; i < E; ++i) b[i] = __float_as_uint(__builtin_fmaf(v[i], s.inv, v[i] * s.low) + 12582912.0f);
     u32x2 r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -132,13 +127,13 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_rows_kernel(FormArgs
         }
         m = MaxOp()(m, amax_of(v[k]));
     }
-    auto write = [&](auto exact, float amax, int8_t *q, float *scale) {
+    auto write = [&](float amax, int8_t *q, float *scale) {
         const I8Scale s = i8_scale(amax);
         q += row * a.Dp;
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
             const int c = (k * lanes + tt) * E;
-            const u32x2 w = i8_codes<decltype(exact)::value>(v[k], s);
+            const u32x2 w = i8_codes(v[k], s);
             if (c < a.Dp) {
                 if (a.nt) store_as<true>(q + c, w);
                 else store_as<false>(q + c, w);
@@ -146,12 +141,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_rows_kernel(FormArgs
         }
         if (tt == 0) scale[row] = s.scale;
     };
-    write(std::bool_constant<ACT == DISCO_ACT_NONE>(), row_max(m, a.lg, slots[0]), a.q, a.scale);
+    write(row_max(m, a.lg, slots[0]), a.q, a.scale);
     if constexpr (ACT != DISCO_ACT_NONE)
         if (a.kq) {
 #pragma unroll
             for (int k = 0; k < KPT; ++k) unpack(px[k], v[k]);
-            write(std::true_type(), row_max(mk, a.lg, slots[1]), a.kq, a.kscale);
+            write(row_max(mk, a.lg, slots[1]), a.kq, a.kscale);
         }
 }
 
@@ -200,24 +195,30 @@ __global__ __launch_bounds__(TH) void quantize_field_kernel(FormArgs a)
     const int turn = lane % a.nv;
     int cg = g + turn;
     if (cg >= a.nv) cg -= a.nv;
-    auto write = [&](auto exact, const uint32_t *m, int8_t *q, float *scale) {
-        I8Scale s[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s[e] = i8_scale(__uint_as_float(m[lane * VEC + e]));
+    auto write = [&](const uint32_t *m, int8_t *q, float *scale) {
+        // four points' scales at a time: all eight take registers that the values need (360x720 points of 2048 channels with gelu, a
+        // checkpoint and two readers: 2097 us with eight, 1920 with four)
+        constexpr int SP = VEC < 4 ? VEC : 4;
         if (holds)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float w[E];
+            for (int e0 = 0; e0 < VEC; e0 += SP) {
+                I8Scale s[SP];
 #pragma unroll
-                for (int j = 0; j < E; ++j) w[j] = v[j][e];
-                *(u32x2 *)(lds + ((lane * VEC + e) * a.nv + cg) * 8) = i8_codes<decltype(exact)::value>(w, s[e]);
+                for (int e = 0; e < SP; ++e) s[e] = i8_scale(__uint_as_float(m[lane * VEC + e0 + e]));
+                if (g == 0) {
+                    float f[SP];
+#pragma unroll
+                    for (int e = 0; e < SP; ++e) f[e] = s[e].scale;
+                    store_f32<float, SP>(scale + pos.n * a.M + pos.m + e0, f);
+                }
+#pragma unroll
+                for (int e = 0; e < SP; ++e) {
+                    float w[E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) w[j] = v[j][e0 + e];
+                    *(u32x2 *)(lds + ((lane * VEC + e0 + e) * a.nv + cg) * 8) = i8_codes(w, s[e]);
+                }
             }
-        if (g == 0) {
-            float f[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f[e] = s[e].scale;
-            store_f32<float, VEC>(scale + pos.n * a.M + pos.m, f);
-        }
         __syncthreads();
         const int half = a.nv >> 1;  // sixteens of a point
         for (int i = t; i < P * half; i += blockDim.x) {
@@ -234,12 +235,12 @@ __global__ __launch_bounds__(TH) void quantize_field_kernel(FormArgs a)
     __syncthreads();
     take(true, mx);
     __syncthreads();
-    write(std::bool_constant<ACT == DISCO_ACT_NONE>(), mx, a.q, a.scale);
+    write(mx, a.q, a.scale);
     if constexpr (ACT != DISCO_ACT_NONE)
         if (a.kq) {
             take(false, mx + P);
             __syncthreads();
-            write(std::true_type(), mx + P, a.kq, a.kscale);
+            write(mx + P, a.kq, a.kscale);
         }
 }
 
@@ -278,8 +279,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void quantize_loop_kernel(FormArgs
         load(c, v);
 #pragma unroll
         for (int j = 0; j < E; ++j) w[j] = act_value<ACT>(v[j]);
-        *(u32x2 *)(a.q + point * a.Dp + c) = i8_codes<ACT == DISCO_ACT_NONE>(w, s);
-        if (a.kq) *(u32x2 *)(a.kq + point * a.Dp + c) = i8_codes<true>(v, k);
+        *(u32x2 *)(a.q + point * a.Dp + c) = i8_codes(w, s);
+        if (a.kq) *(u32x2 *)(a.kq + point * a.Dp + c) = i8_codes(v, k);
     }
     if (g == 0) {
         a.scale[point] = s.scale;

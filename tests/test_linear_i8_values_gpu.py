@@ -63,3 +63,19 @@ def test_gelu_slope_in_the_lower_tail(layout):
     # R - t / sqrt(2 pi): the polynomial, six of its last steps and of the difference; the exponential and two products
     err = e * (9.1e-8 * (1 + t * t / 8) * R + 8 * V * (R + d)) + z.abs() * V * (1.5 * t * t + 6) + V * want.abs() * (v > 0)
     assert bool(((gx - want).abs() <= (err + u_of("bf16") * want.abs()) * 1.01).all())
+
+
+@pytest.mark.parametrize("layout,C", [("rows", 128), ("rows", 2064), ("rows", 33000), ("field", 128), ("field", 2064)])
+@pytest.mark.parametrize("act", [None, "gelu", "silu"])
+def test_codes_are_the_quotients_by_the_stored_scale(layout, C, act):
+    # From 17 on both functions give their argument itself in fp32, so the codes are those of x.  A point's largest value is 127 times
+    # a scale of its own, and its other values lie at (k + 1/2) scale and beside it: exact ties go to the even code.
+    P = 64
+    scale = torch.tensor([3.0, 7.0, 11.0, 1.0, 5.5, 9.0, 13.0, 1.3, 2.7, 6.1], device="cuda").repeat(7)[:P]
+    k = torch.randint(17, 126, (P, C), generator=gen(1), device="cuda").float()
+    x = ((k + 0.5) * scale[:, None]) * (1 + torch.randint(-1, 2, (P, C), generator=gen(2), device="cuda") * 2.0 ** -23)
+    x[:, 5] = 127 * scale
+    q, s = sgc.disco_quantize_i8(points_as(x, layout), act=act)
+    s32 = x.cpu().abs().amax(1) / 127
+    assert torch.equal(s.reshape(P).cpu(), s32)
+    assert torch.equal(q.reshape(P, -1)[:, :C].cpu().float(), torch.round(x.cpu() / s32[:, None]))
