@@ -439,11 +439,15 @@ def _act_code(act) -> int:
         raise DiscoError(1, "act must be None, 'gelu' or 'silu'") from None
 
 
-def _channels(channels) -> int:
+def _channels(channels, given, axis, name) -> int:
+    """`channels` (-1: not asked for), which a given output has to have at `axis`."""
     if channels is None:
         return -1
     if channels < 0:
         raise DiscoError(2, "the number of channels is out of range")
+    shape = getattr(given, "shape", ())
+    if -len(shape) <= axis < len(shape) and shape[axis] != channels:  # (an axis out of range is the library's to refuse)
+        raise DiscoError(2, f"{name} has {shape[axis]} channels, {channels} were asked for")
     return channels
 
 
@@ -460,7 +464,7 @@ def disco_quantize_i8(x, act=None, keep=False, axis=1, q=None, scale=None, kept=
 def disco_dequantize_i8(q, scale, channels=None, dtype=None, axis=1, out=None):
     """out = q * scale in `dtype` (default bf16, or the given out's), `channels` of them (default: all of q's) at `axis`."""
     code = DISCO_BF16 if dtype is None else _data_code(dtype, out)
-    return (_bind or _binding()).dequantize_i8(q, scale, _channels(channels), code, axis, out)
+    return (_bind or _binding()).dequantize_i8(q, scale, _channels(channels, out, axis, "out"), code, axis, out)
 
 
 def disco_linear_i8(q, scale, w, wscale, bias=None, dtype=None, axis=1, out=None):
@@ -477,7 +481,8 @@ def disco_linear_i8_bwd_input(gy, w, wscale, channels=None, act=None, kept=None,
 
     With act, kept and kept_scale the gradient of what act was taken of before the product: times act'(kept kept_scale).
     `channels` is the input's number of channels (default: all of w's)."""
-    return (_bind or _binding()).linear_i8_bwd_input(gy, w, wscale, _channels(channels), _act_code(act), kept, kept_scale, axis, gx)
+    return (_bind or _binding()).linear_i8_bwd_input(gy, w, wscale, _channels(channels, gx, axis, "gx"), _act_code(act), kept, kept_scale,
+                                                       axis, gx)
 
 
 def disco_linear_i8_bwd_weight_workspace(gy, channels, bias=False, axis=1) -> int:
@@ -490,4 +495,5 @@ def disco_linear_i8_bwd_weight(gy, q, scale, channels=None, bias=False, axis=1, 
 
     q, scale: the 8-bit input that the forward took; gy has its Co channels at `axis`.  The workspace (a uint8 device
     tensor) is allocated here when not given."""
-    return (_bind or _binding()).linear_i8_bwd_weight(gy, q, scale, _channels(channels), bias or db is not None, axis, dw, db, workspace)
+    return (_bind or _binding()).linear_i8_bwd_weight(gy, q, scale, _channels(channels, dw, -1, "dw"), bias or db is not None, axis, dw, db,
+                                                        workspace)
