@@ -79,3 +79,53 @@ def test_codes_are_the_quotients_by_the_stored_scale(layout, C, act):
     s32 = x.cpu().abs().amax(1) / 127
     assert torch.equal(s.reshape(P).cpu(), s32)
     assert torch.equal(q.reshape(P, -1)[:, :C].cpu().float(), torch.round(x.cpu() / s32[:, None]))
+
+
+# one step, several steps a split, many splits; tiles of 256 x 256, 128 x 128 and 32 x 256; shared sums of db; whole and ragged planes
+WEIGHTS = [((64,), 256, 256), ((1000,), 48, 300), ((33000,), 300, 40), ((70000,), 140, 130), ((70001,), 512, 1030), ((200000,), 256, 256), ((130000,), 20, 600),
+           ((3, 9, 13), 80, 73), ((2, 181, 360), 200, 48), ((2, 300, 333), 256, 256), ((2, 300, 334), 256, 512), ((3, 285, 291), 8, 307), ((1, 361, 720), 600, 260)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("points,C,Co", WEIGHTS, ids=str)
+def test_bwd_weight_of_whole_numbers(points, C, Co, dt):
+    # gy in eighths, codes and scales of 1/2, 1 and 2: every term is a whole number of at most 1016 sixteenths, so fp32 sums of up to
+    # 16,000 points (no split here is longer) are exact in any order, the fp64 ones over the splits too, and the results are the true
+    # sums rounded once.  A point that is left out or met twice shows.
+    P = 1
+    for n in points:
+        P *= n
+    g = torch.randint(-2, 3, (P, Co), generator=gen(1), device="cuda").double() / 8
+    q = torch.zeros((P, -(-C // 16) * 16), dtype=torch.int8, device="cuda")
+    q[:, :C] = torch.randint(-127, 128, (P, C), generator=gen(2), device="cuda")
+    s = torch.tensor([0.5, 1.0, 2.0], device="cuda")[torch.randint(0, 3, (P,), generator=gen(3), device="cuda")]
+    gy = g.to(DT[dt]).view(tuple(points) + (Co,)).movedim(-1, 1).contiguous()
+    assert gy.shape == shape_of(points, Co)
+    x = q[:, :C].double() * s.double()[:, None]
+    want = g.t() @ x
+    dw, db = sgc.disco_linear_i8_bwd_weight(gy, q.view(tuple(points) + (-1,)), s.view(points), channels=C, bias=True)
+    assert torch.equal(dw, want.to(DT[dt])) and torch.equal(db, g.sum(0).to(DT[dt]))
+    assert torch.equal(dw, sgc.disco_linear_i8_bwd_weight(gy, q.view(tuple(points) + (-1,)), s.view(points), channels=C))
+    # the comparison sees one point in the middle
+    less = want - g[P // 2][:, None] * x[P // 2][None, :]
+    assert not torch.equal(less.to(DT[dt]), want.to(DT[dt]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("points,C,Co", [((70000,), 140, 130), ((200000,), 256, 256), ((2, 300, 333), 256, 256), ((2, 181, 360), 200, 160)], ids=str)
+def test_bwd_weight_error_of_its_norm(points, C, Co, dt):
+    # Rounding a value to 16 bits is off by 0.425 u of it in the root mean square (uniform within a step, over mantissas spread as
+    # their logarithms).  Each term passes one such rounding and the result one, independent of each other and of the terms' signs, so
+    # the error's norm is 0.425 sqrt(2) u = 0.6 u of the result's; 0.75 u leaves out no more than a point in 300,000 (bf16).
+    # db: its rounding alone, at most u.  fp32 sums of up to n steps of 16 points: sqrt(n) V, 1e-5 here.
+    P = 1
+    for n in points:
+        P *= n
+    gy = (torch.randn(shape_of(points, Co), generator=gen(1), device="cuda") / 2).to(DT[dt])
+    x = torch.randn((P, C), generator=gen(2), device="cuda")
+    q, s = sgc.disco_quantize_i8(x)
+    v, g = q[:, :C].double() * s.double()[:, None], rows(gy)
+    dw, db = sgc.disco_linear_i8_bwd_weight(gy, q.view(tuple(points) + (-1,)), s.view(points), channels=C, bias=True)
+    want, wb = g.t() @ v, g.sum(0)
+    assert float((dw.double() - want).norm()) <= (0.75 * u_of(dt) + 1e-5) * float(want.norm())
+    assert float((db.double() - wb).norm()) <= (u_of(dt) + 1e-5) * float(wb.norm())
