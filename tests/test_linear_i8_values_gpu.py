@@ -129,3 +129,28 @@ def test_bwd_weight_error_of_its_norm(points, C, Co, dt):
     want, wb = g.t() @ v, g.sum(0)
     assert float((dw.double() - want).norm()) <= (0.75 * u_of(dt) + 1e-5) * float(want.norm())
     assert float((db.double() - wb).norm()) <= (u_of(dt) + 1e-5) * float(wb.norm())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("points,C,Co", [((2, 721, 1440), 256, 256), ((2, 721, 1440), 48, 70), ((2, 721, 1440), 100, 70), ((2, 721, 1440), 300, 65), ((1, 512, 1024), 256, 160),
+                                         ((3, 361, 720), 130, 257)], ids=str)
+def test_linear_over_large_fields(points, C, Co, dt):
+    # more than 128 MiB of output: the weights stay in registers, for every bucket of channels; planes that end half way through
+    # a tile of 64 points (721 x 1440 and 361 x 720), so a tile crosses from one plane to the next
+    P = points[0] * points[1] * points[2]
+    q = torch.zeros((P, -(-C // 16) * 16), dtype=torch.int8, device="cuda")
+    q[:, :C] = torch.randint(-127, 128, (P, C), generator=gen(1), device="cuda", dtype=torch.int8)
+    w = torch.zeros((Co, q.shape[1]), dtype=torch.int8, device="cuda")
+    w[:, :C] = torch.randint(-127, 128, (Co, C), generator=gen(2), device="cuda", dtype=torch.int8)
+    s = torch.rand(P, generator=gen(3), device="cuda") * 0.02 + 0.005
+    ws = (torch.rand(Co, generator=gen(4), device="cuda") + 0.5) / (127 * C ** 0.5)
+    bias = torch.randn(Co, generator=gen(5), device="cuda")
+    y = sgc.disco_linear_i8(q.view(points + (-1,)), s.view(points), w, ws, bias=bias, dtype=DT[dt])
+    assert y.shape == shape_of(points, Co) and y.numel() * 2 > 128 << 20
+    M = points[1] * points[2]
+    for b in range(points[0]):
+        t = (q[b * M:(b + 1) * M].double() @ w.double().t()).mul_(s[b * M:(b + 1) * M].double()[:, None]).mul_(ws.double())
+        want = t + bias.double()
+        # the sum's conversion and two scales, the bias, the output's rounding (fp16's subnormals: half a step)
+        tol = 1.01 * (3 * V * t.abs() + (V + u_of(dt)) * want.abs()) + 2.0 ** -25
+        assert bool(((y[b].reshape(Co, M).t().double() - want).abs() <= tol).all()), b
