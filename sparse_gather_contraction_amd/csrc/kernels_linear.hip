@@ -178,17 +178,7 @@ __global__ __launch_bounds__(L::kThreads, 2) void linear_i8_kernel(LinArgs a)
 // ---------------------------------------------------------------- many points, up to 512 channels
 
 // The weights stay in the matrix cores' registers: a wave holds 64 output channels with all their input channels, a workgroup
-// of four 256 of them, and walks a stream of points, PT at a time, which pass through a ring of tiles in LDS.
-template <int K_>
-struct LStay {
-    static constexpr int K = K_;                        // channels, padded
-    static constexpr int PT = K == 512 ? 32 : 64;       // points of a tile
-    static constexpr int RING = K >= 256 ? 3 : 4;
-    static constexpr int kTile = PT * K, kStage = kTile + 4 * 256;   // each wave brings its own copy of the scales
-    static constexpr int LOADS = kTile / 16 / 256 + 1;
-};
-constexpr int kStayChannels = 256;   // output channels of a workgroup
-
+// of four 256 of them, and walks a stream of points, PT at a time, which pass through a ring of tiles in LDS (LStay).
 struct StayArgs {
     LinArgs l;
     int32_t nt;                      // stores past the caches

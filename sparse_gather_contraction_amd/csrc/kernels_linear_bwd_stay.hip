@@ -20,19 +20,6 @@ namespace disco {
 
 namespace {
 
-// KB: bytes of a point's gradients, padded (two an output channel).  KEPT: a checkpoint comes with them.
-template <int KB_, bool KEPT>
-struct GStay {
-    static constexpr int KB = KB_;
-    static constexpr int FW = KB == 1024 ? 1 : 2;            // 32 channels each, of a wave
-    static constexpr int CW = 32 * FW, CB = 4 * CW;          // channels of a wave, of a workgroup
-    static constexpr int PT = KB >= 512 ? 32 : 64;           // points of a tile
-    static constexpr int RING = KB == 512 || (KB <= 256 && !KEPT) ? 3 : 2;
-    static constexpr int kTile = PT * KB, kKept = KEPT ? PT * CB : 0;
-    static constexpr int kStage = kTile + kKept + (KEPT ? 4 * 256 : 0);   // each wave brings its own copy of the scales
-    static constexpr int LOADS = kTile / 16 / 256, KLOADS = kKept / 16 / 256;
-};
-
 struct GStayArgs {
     const uint16_t *gy;
     const int8_t *w, *kept;

@@ -4,8 +4,9 @@
 //
 // Walks the form's writer and reader as the kernels do, for many shapes and element sizes (every access inside its tensor,
 // every element and code met, the LDS indexes inside what a launch asks for, a tile's codes read where they were written),
-// and checks the division by a product, the products' LDS layouts, the map of workgroups to tiles and the splits of the
-// weight's gradient.  Prints the number of geometries checked.
+// and checks the division by a product, the products' LDS layouts, the ring of the kernels that hold their weights in registers
+// (direct loads and the reads of a tile), the map of workgroups to tiles and the splits of the weight's gradient.  Prints the
+// number of geometries checked.
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
@@ -122,6 +123,89 @@ static void check_slots(int rows)
         }
 }
 
+// One stage of a ring: what each 16 bytes hold, by the direct loads (instruction i of 256 threads writes slots 256 i ..), as
+// point << 20 | first byte of the point's run; -1: nothing.
+struct Stage {
+    std::vector<int64_t> at;
+    int64_t size;
+    explicit Stage(int bytes) : at((size_t)bytes / 16, -1), size(bytes) {}
+    template <int K>
+    void load(int base, int loads, int points, const char *what)
+    {
+        for (int i = 0; i < loads; ++i)
+            for (int tid = 0; tid < 256; ++tid) {
+                const int s = i * 256 + tid, row = s / (K / 16), lds = base + 16 * (i * 256 + (tid >> 6) * 64) + 16 * (tid & 63);
+                if (lds + 16 > size || at[(size_t)lds / 16] >= 0 || row >= points) fail(what, s, row, lds, K);
+                at[(size_t)lds / 16] = (int64_t)row << 20 | 16 * lin_piece<K>(s);
+            }
+    }
+    // n bytes at `lds` are the bytes `byte` .. of point `p`
+    void read(int64_t lds, int n, int p, int byte, const char *what) const
+    {
+        if (lds < 0 || lds % n || lds + n > size || at[(size_t)lds / 16] != ((int64_t)p << 20 | (byte & ~15)) || lds % 16 != byte % 16) fail(what, lds, p, byte, n);
+    }
+    // the four waves' copies of the scales: 64 lanes of 4 bytes each, behind all else
+    void scales(int base, int points)
+    {
+        for (int w = 0; w < 4; ++w) {
+            for (int b = 0; b < 256; b += 16)
+                if (base + 256 * w + b + 16 > size || at[(size_t)(base + 256 * w + b) / 16] >= 0) fail("scales", base, w, b, 0);
+                else at[(size_t)(base + 256 * w + b) / 16] = -2 - w;
+            if (4 * points > 256) fail("scales of a tile", points, w, 0, 0);
+        }
+        if (base + 4 * 256 != size) fail("stage", base, (int)size, 0, 0);
+    }
+};
+
+// A full tile of the product: whole rows of K bytes, then the reads of its operands.
+template <int K>
+static int check_stay()
+{
+    typedef LStay<K> L;
+    Stage st(L::kStage);
+    st.load<K>(0, L::LOADS - 1, L::PT, "product's tile");
+    st.scales(L::kTile, L::PT);
+    for (int j = 0; j < L::PT; j += 32)
+        for (int k = 0; k < K / 32; ++k)
+            for (int lane = 0; lane < 64; ++lane) st.read(lin_at<K>(j + (lane & 31), 2 * k + (lane >> 5)), 16, j + (lane & 31), 32 * k + 16 * (lane >> 5), "product's operand");
+    if (2 * (L::RING * L::kStage + 2 * kStayChannels * 4) > 160 * 1024) fail("two workgroups' LDS", K, L::RING, L::kStage, 0);
+    return 1;
+}
+
+// And of the input's gradient, with the checkpoint of a lane's four neighbouring channels.
+template <int KB, bool KEPT>
+static int check_bwd_stay()
+{
+    typedef GStay<KB, KEPT> L;
+    Stage st(L::kStage);
+    st.load<KB>(0, L::LOADS, L::PT, "gradient's tile");
+    if (KEPT) {
+        // (a byte of the checkpoint is told from one of the gradients by its point: 32 points or 64 further on)
+        Stage kt(L::kKept);
+        kt.load<L::CB>(0, L::KLOADS, L::PT, "checkpoint's tile");
+        for (int64_t i = 0; i < (int64_t)kt.at.size(); ++i) {
+            if (st.at[(size_t)(L::kTile / 16 + i)] >= 0 || kt.at[(size_t)i] < 0) fail("checkpoint's place", i, KB, 0, 0);
+            st.at[(size_t)(L::kTile / 16 + i)] = kt.at[(size_t)i] + ((int64_t)L::PT << 20);
+        }
+        st.scales(L::kTile + L::kKept, L::PT);
+    }
+    for (int j = 0; j < L::PT; j += 32)
+        for (int lane = 0; lane < 64; ++lane) {
+            const int r = lane & 31, h = lane >> 5;
+            for (int k = 0; k < KB / 32; ++k) st.read(lin_at<KB>(j + r, 2 * k + h), 16, j + r, 32 * k + 16 * h, "gradient's operand");
+            for (int wave = 0; KEPT && wave < 4; ++wave)
+                for (int i = 0; i < L::FW; ++i)
+                    for (int g = 0; g < 4; ++g) {
+                        const int col = L::CW * wave + 32 * i + 8 * g + 4 * h;
+                        st.read(L::kTile + lin_at<L::CB>(j + r, col >> 4) + (col & 15), 4, L::PT + j + r, col, "checkpoint");
+                    }
+        }
+    for (int64_t v : st.at)
+        if (v == -1) fail("a place of the stage that nothing fills", KB, KEPT, 0, 0);
+    if (2 * L::RING * L::kStage > 160 * 1024) fail("two workgroups' LDS", KB, L::RING, L::kStage, KEPT);
+    return 1;
+}
+
 int main()
 {
     int n = 0;
@@ -159,6 +243,10 @@ int main()
         check_slots<256>(rows);
         check_slots<512>(rows);
     }
+    check_slots<1024>(32);
+    n += check_stay<64>() + check_stay<128>() + check_stay<256>() + check_stay<512>();
+    n += check_bwd_stay<128, false>() + check_bwd_stay<256, false>() + check_bwd_stay<512, false>() + check_bwd_stay<1024, false>();
+    n += check_bwd_stay<128, true>() + check_bwd_stay<256, true>() + check_bwd_stay<512, true>() + check_bwd_stay<1024, true>();
     for (int64_t total : {1, 7, 8, 9, 255, 256, 1000, 8104}) {
         std::vector<int> met((size_t)total, 0);
         for (int64_t i = 0; i < total; ++i) {

@@ -150,7 +150,7 @@ DISCO_HD void lin_tile(int64_t i, int64_t n, int32_t fast, int32_t *a, int32_t *
     *a = (int32_t)(t - (int64_t)*b * fast);
 }
 
-// LDS of a tile of 8-bit rows, K channels (64 to 512) a step: slot i (16 bytes) holds row i / (K / 16), piece lin_piece(i).
+// LDS of a tile of rows of K bytes (64 to 1024; 8-bit channels of a step, or gradients of two bytes): slot i (16 bytes) holds row i / (K / 16), piece lin_piece(i).
 // The pieces of a row are turned by the row, so that sixteen rows' equal pieces lie in sixteen different banks.
 template <int K>
 DISCO_HD int lin_turn(int row) { return K == 64 ? row >> 2 & 3 : K == 128 ? row >> 1 & 7 : row & 15; }
@@ -158,6 +158,34 @@ template <int K>
 DISCO_HD int lin_piece(int slot) { return (slot % (K / 16)) ^ lin_turn<K>(slot / (K / 16)); }
 template <int K>
 DISCO_HD int lin_at(int row, int piece) { return row * K + 16 * (piece ^ lin_turn<K>(row)); }
+
+// The weights in registers: tiles of PT points pass through a ring in LDS by direct loads, four waves of 256 threads.  A tile's
+// slot i (16 bytes) holds what lin_piece says; behind it each wave's own copy of the points' scales.
+//
+// The product: K channels, padded.
+template <int K_>
+struct LStay {
+    static constexpr int K = K_;
+    static constexpr int PT = K == 512 ? 32 : 64;       // points of a tile
+    static constexpr int RING = K >= 256 ? 3 : 4;
+    static constexpr int kTile = PT * K, kStage = kTile + 4 * 256;
+    static constexpr int LOADS = kTile / 16 / 256 + 1;  // direct loads of a thread and tile
+};
+constexpr int kStayChannels = 256;   // output channels of a workgroup
+
+// The input's gradient.  KB: bytes of a point's gradients, padded (two an output channel).  KEPT: a checkpoint comes with them,
+// between the tile and the scales.
+template <int KB_, bool KEPT>
+struct GStay {
+    static constexpr int KB = KB_;
+    static constexpr int FW = KB == 1024 ? 1 : 2;            // 32 channels each, of a wave
+    static constexpr int CW = 32 * FW, CB = 4 * CW;          // channels of a wave, of a workgroup
+    static constexpr int PT = KB >= 512 ? 32 : 64;           // points of a tile
+    static constexpr int RING = KB == 512 || (KB <= 256 && !KEPT) ? 3 : 2;
+    static constexpr int kTile = PT * KB, kKept = KEPT ? PT * CB : 0;
+    static constexpr int kStage = kTile + kKept + (KEPT ? 4 * 256 : 0);
+    static constexpr int LOADS = kTile / 16 / 256, KLOADS = kKept / 16 / 256;
+};
 
 // LDS of an operand staged [r][n], rows of N 16-bit elements: the 32-byte piece c of row r lies at piece
 // c ^ (2 (r % 4) + r / 8 % 2).  A transposing read takes rows r .. r + 3 of two neighbouring pieces, and of rows r + 8 ..
