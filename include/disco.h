@@ -292,11 +292,12 @@ disco_status disco_clip_grads(int64_t n, const disco_tensor *grads, float max_no
  * 16-byte aligned.  scale: F32, the tensor's shape without the channel axis.  A point that holds a NaN or an infinity has
  * scale NaN and q 0.  A weight (Co, C) takes the same form over its last axis: w (Co, Cp), wscale (Co).
  * At most 2^31 - 4096 points (and output channels), at most 131056 padded channels in a product (so that its sums, also
- * of q = -128, stay below 2^31). */
+ * of q = -128, stay below 2^31); a call that needs more threads than a launch has (2^32 - 1) is refused too. */
 
 /* The form of act(x).  x: F32, BF16 or F16, 1 to 5 dimensions.  kept, kept_scale: both NULL, or the form of x itself, the
  * checkpoint that disco_linear_i8_bwd_input takes the function's slope from (only with an activation function: without
- * one it is q).  act is evaluated in fp32. */
+ * one it is q).  act is evaluated in fp32, off by at most 2^-20 (1 + x^2 / 8) of its size for gelu and 2^-23 (|x| + 4) for
+ * silu; where e^(-x^2/2) or e^x leaves fp32's range (below -13.2 and -87.3) it is 0. */
 disco_status disco_quantize_i8(const disco_tensor *x, disco_act act, int axis, disco_tensor *q, disco_tensor *scale,
                                disco_tensor *kept, disco_tensor *kept_scale, void *stream);
 
@@ -317,7 +318,9 @@ disco_status disco_linear_i8(const disco_tensor *q, const disco_tensor *scale, c
  *   gx[p,c] = act'(kept[p,c] kept_scale[p]) sum_o gy[p,o] wscale[o] w[o,c]
  * gy, gx: BF16 or F16, both alike, dense, channels at `axis` (Co in gy, C in gx); w (Co, Cp), wscale (Co) as above, C
  * padded to 16 giving Cp; kept (points..., Cp) and kept_scale (points...) with an activation function, NULL without one.
- * wscale w is rounded to the data type (RNE), the sum is fp32. */
+ * wscale w is rounded to the data type (RNE), the sum is fp32.  In fp16 that operand has fp16's range: infinite from 65520
+ * on, fewer bits below 2^-14.  act' is off by at most 2^-20 for gelu (below -2 by 2^-19 (1 + x^2 / 8) of its size) and 2^-19
+ * for silu. */
 disco_status disco_linear_i8_bwd_input(const disco_tensor *gy, const disco_tensor *w, const disco_tensor *wscale,
                                        disco_act act, const disco_tensor *kept, const disco_tensor *kept_scale,
                                        int axis, disco_tensor *gx, void *stream);
@@ -326,7 +329,9 @@ disco_status disco_linear_i8_bwd_input(const disco_tensor *gy, const disco_tenso
  *   dw[o,c] = sum_p gy[p,o] scale[p] q[p,c],   db[o] = sum_p gy[p,o]
  * gy: BF16 or F16, dense, its Co channels at `axis`; q (points..., Cp), scale (points...): the 8-bit operand that the
  * forward took; dw (Co, C) and db (Co) or NULL, of gy's type.  scale q is rounded to the data type (RNE) as the reader
- * writes it; sums are fp32 in runs of points and fp64 over the runs, in a fixed order.  With no points both are zeros.
+ * writes it, in fp16 with fp16's range as above: a form of values from 65520 on, made from bf16 or fp32, gives infinities
+ * there.  Sums are fp32 in runs of points and fp64 over the runs, in a fixed order; a dw that fills the GPU by itself (more
+ * than 2^23 elements) is one run of all points, whose rounding errors grow with their number.  With no points both are zeros.
  * `workspace` is caller-owned device memory (16-byte aligned) of at least the size that
  * disco_linear_i8_bwd_weight_workspace reports for these tensors (their data is not read; db: whether there is one); its
  * contents on entry are ignored; may be NULL where the size is 0.  Calls sharing one workspace must not overlap. */

@@ -154,3 +154,30 @@ def test_linear_over_large_fields(points, C, Co, dt):
         # the sum's conversion and two scales, the bias, the output's rounding (fp16's subnormals: half a step)
         tol = 1.01 * (3 * V * t.abs() + (V + u_of(dt)) * want.abs()) + 2.0 ** -25
         assert bool(((y[b].reshape(Co, M).t().double() - want).abs() <= tol).all()), b
+
+
+@pytest.mark.parametrize("layout,C", [("rows", 1), ("rows", 200), ("field", 40)])
+def test_silu_of_points_in_the_lower_tail(layout, C):
+    # as for gelu, down to where e^x leaves fp32's range
+    P = 1000
+    top = -2 - 85 * torch.arange(P, device="cuda") / P
+    x = top[:, None] - torch.rand((P, C), generator=gen(1), device="cuda") / 4
+    q, s = sgc.disco_quantize_i8(points_as(x, layout), act="silu")
+    q, s, v = q.reshape(P, -1)[:, :C].double(), s.reshape(P).double(), x.double()
+    g = v / (1 + torch.exp(-v))
+    # the exponent's argument (a constant's rounding and a product's), the exponential, the sum, the reciprocal and the product
+    err = g.abs() * V * (2 * v.abs() + 8)
+    want = (g.abs().amax(1) / 127).clamp(min=2.0 ** -126)
+    assert bool(((s - want).abs() <= err.amax(1) / 127 + V * want * 1.01).all())
+    assert bool(((q * s[:, None] - g).abs() <= s[:, None] * (0.5 + 128 * V) + err).all())
+
+
+def test_functions_beyond_their_tails():
+    # from where the exponential leaves fp32's range on both functions are 0, whatever the size of what they are taken of
+    x = torch.tensor([-13.3, -14.5, -20.0, -1e4, -1e30, -3.4e38], device="cuda").view(-1, 1)
+    for act, shift in (("gelu", 0.0), ("silu", -76.0)):
+        q, s, k, ks = sgc.disco_quantize_i8(x + shift, act=act, keep=True)
+        assert bool((s == 2.0 ** -126).all()) and bool((q == 0).all()) and bool((k[:, 0] == -127).all())
+        w, ws = torch.ones((1, 16), dtype=torch.int8, device="cuda"), torch.ones(1, device="cuda")
+        gx = sgc.disco_linear_i8_bwd_input(torch.ones((6, 1), dtype=torch.bfloat16, device="cuda"), w, ws, channels=1, act=act, kept=k, kept_scale=ks)
+        assert bool((gx.abs() <= 2.0 ** -115).all())
