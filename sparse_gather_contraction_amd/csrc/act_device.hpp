@@ -10,7 +10,9 @@ namespace disco {
 // t = |v|, up to 14.5 where e is 0 in fp32.  The coefficients are a least-maximum fit on [0, 13.2] in fp64 of the error relative
 // to R, weighted by 1 / (1 + t^2 / 8): off by 9.1e-8 (1 + t^2 / 8) of R.  With e's argument rounded (three roundings of
 // t^2 / 2) the tail is off by a part in 2.4e6 near 0, 6e5 at 4 and 1e5 at 12: a point whose values all lie in it has a scale and codes
-// as good as any other's.  A NaN stays one.
+// as good as any other's.  A NaN stays one.  (1/2 plus an odd polynomial, off by 2.4e-7 of 1 anywhere, has no such tail and is
+// hardly faster: the 8-bit form of 259200x2048 bf16 with gelu and a checkpoint, and two readers, 904 us against 921; input's
+// gradients through its slope, off by 5.1e-7, 941 us against 934 at 2048 from 512.)
 struct NormalTail {
     float t, e, p;
 };

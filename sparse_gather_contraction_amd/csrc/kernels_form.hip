@@ -5,8 +5,9 @@
 //
 // Everything between the load and q is fp32, the quotient by the scale as it is stored, so that q scale is the nearest
 // such value to v.  Memory bounds the plain writer and the reader (2x256x721x1440 bf16: 300-316 and 343 us, 5.3 and 4.7 TB/s; rows
-// of 2048 bf16 read back at 6.1), the vector units the writer with gelu and a checkpoint (259200x2048: 389-481 us).  A point that
-// holds a NaN or an infinity has scale NaN and q 0: what is computed from it is NaN.
+// of 2048 bf16 read back at 6.1), the vector units the writer with gelu and a checkpoint (259200x2048: 479-495 us; the function's
+// exponential and reciprocal, and two quantisations of each value).  A point that holds a NaN or an infinity has scale NaN and
+// q 0: what is computed from it is NaN.
 #include "act_device.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"

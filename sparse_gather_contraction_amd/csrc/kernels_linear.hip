@@ -8,9 +8,10 @@
 // Both operands lie with their channels together, so a tile of rows is 64-byte pieces for the matrix cores' 8-bit
 // instruction (v_mfma_i32_32x32x32_i8), brought by direct loads to LDS.  Rows and fields differ in which operand the
 // instruction takes first: a lane holds four neighbouring values of its first operand's axis, which is the one that lies
-// together in the output, the output channels (rows) or the points (fields).  Few channels are bound by the output's bytes
-// (259200 rows, 512 to 2048 bf16: 374 us, 3.2 TB/s; 2x256x721x1440 from 256: 382), many by the matrix cores (8192^3: 551 us,
-// 2.0 Pop/s), few points by the weights' (16 rows, 8192 to 8192: 17.5 us, 3.9 TB/s) or the launch.
+// together in the output, the output channels (rows) or the points (fields).  With few channels a wave's products and its
+// writes, from one set of accumulators, take turns (259200 rows, 512 to 2048 bf16: 376 us, 3.2 TB/s and the matrix cores 38 %
+// busy; 2x256x721x1440 from 256: 380); many are bound by the matrix cores (8192^3: 558 us, 2.0 Pop/s), few points by the
+// weights' bytes (16 rows, 8192 to 8192: 17.4 us, 3.9 TB/s) or the launch.
 #include "kernels.hpp"
 #include "linear.hpp"
 #include "linear_device.hpp"

@@ -69,7 +69,6 @@ __device__ __forceinline__ bf16x8 frag_across(const unsigned char *op, int n0, i
     const int n = n0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), r = r0 + 8 * (lane >> 5) + ((lane >> 2) & 3);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(op + bwd_across<N>(r, n)));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(op + bwd_across<N>(r + 4, n)));
-    typedef short s16x8 __attribute__((ext_vector_type(8)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 

@@ -6,8 +6,8 @@
 // the matrix cores' registers: a wave holds 64 input channels (32 beyond 256 output channels), a workgroup of four walks a
 // stream of points whose gradients and checkpoints pass through a ring of tiles in LDS by direct loads.  In tiles, a third of
 // the vector instructions form the weights again for every 256 points, and with gelu's slope they, not the matrix cores, are
-// the bound.  bf16, us against tiles: 259200 rows, 2048 from 512, 945 against 1092 with gelu, 709 against 763 alone; 1000000
-// rows with gelu, 512 from 128, 557 against 664, 256 from 64, 240 against 306; 2076480 rows, 256 from 256, 484 against 519.
+// the bound.  bf16, us against tiles: 259200 rows, 2048 from 512, 935 against 1067 with gelu, 700 against 743 alone; 1000000
+// rows with gelu, 512 from 128, 523 against 696, 256 from 64, 230 against 315; 2076480 rows, 256 from 256, 468 against 535.
 // With gelu at 2048 from 512 the matrix cores work a quarter of the time (0.58 PFLOP/s) and half of the waves' time is waits.
 #include <type_traits>
 

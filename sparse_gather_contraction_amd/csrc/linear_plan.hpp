@@ -57,8 +57,8 @@ struct FormGeom {
 
 constexpr int kFormChannels = 8;                 // channels of a thread's vector
 // Fields: workgroups of 512 threads, two or three of them a CU, so that the loads of one run beside the turn and the stores
-// of another (2x256x721x1440 bf16: writer 340 us, with 1024 threads and runs twice as long 407; reader 326 and 310;
-// 80x721x1440 both 108 and 123); 1024 where that many hold the channels of a few points at least.
+// of another (2x256x721x1440 bf16: writer 302 us, with 1024 threads and runs twice as long 389; reader 349 and 331;
+// 80x721x1440 both 90 and 105); 1024 where that many hold the channels of a few points at least.
 constexpr int kFormThreads = 512;
 
 inline FormGeom form_geom(int64_t N, int64_t D, int64_t M, int esz)
